@@ -81,6 +81,12 @@ typedef enum {
   SFP8_E5M2 = 4   /* OCP e5m2: max 57344                          */
 } sfp8_dtype;
 
+/* Activation of a gated feed-forward block. */
+typedef enum {
+  SFP8_ACT_SILU = 0,  /* g / (1 + exp(-g))                                      */
+  SFP8_ACT_GELU = 1   /* tanh form: g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) */
+} sfp8_activation;
+
 /* Bits of the device status word. */
 #define SFP8_DEVICE_TIMEOUT     0x1u  /* a bounded mbarrier wait gave up     */
 #define SFP8_DEVICE_CHECK_FAIL  0x2u  /* a device-side check failed          */
@@ -454,6 +460,52 @@ sfp8_status sfp8_sparse_linear_quant_chained(const void* x, sfp8_dtype x_dtype, 
  * and without a device).  Host-only query.
  */
 int sfp8_sparse_linear_quant_fusable(int64_t m, int64_t n, int64_t k);
+
+/*
+ * Gated feed-forward block: both projections, the activation and the product
+ * in one GEMM over one compressed weight,
+ *     gate[m, j] = s_a[m] * s_w[2j]     * sum_k A_q[m, k] W_q[2j, k]     + bias[j]
+ *     up[m, j]   = s_a[m] * s_w[2j + 1] * sum_k A_q[m, k] W_q[2j + 1, k] + bias[n + j]
+ *     h[m, j]    = bf16_RNE( act(gate[m, j]) * up[m, j] )
+ * gate and up stay in fp32 and are not stored.  (The pages apply the sparse
+ * linear to Llama's MLP, whose gate and up projections are this pair; the
+ * fused block has no counterpart there.)
+ *
+ * sfp8_prepare_gated_weight_24 makes the weight: w_gate and w_up [n, k] are
+ * pruned, quantised and compressed as by sfp8_prepare_weight_24 into ONE
+ * packed weight of 2n rows that alternate gate 0, up 0, gate 1, up 1, ...
+ * (sfp8_compressed_bytes(2n, k) bytes, s_w [2n] in the same order).  Both
+ * weights have the same type and the same row stride ld_w.
+ *
+ * sfp8_gated_linear takes the quantised activation; sfp8_gated_linear_quant
+ * quantises x [m, k] first in the same call (a_q and s_a are written: the
+ * 8-bit checkpoint that sfp8_gated_linear_backward takes), like
+ * sfp8_sparse_linear_quant.  Both use the work split of a sparse linear with
+ * 2n rows: the table of sfp8_sparse_linear_set_algo(m, 2n, k) applies.
+ *
+ *  n       hidden units (0 <= n < 2^30); packed and s_w hold 2n rows.
+ *  act     SFP8_ACT_SILU or SFP8_ACT_GELU.
+ *  bias    device, [2n] bf16: gate's n values, then up's; or NULL.
+ *  h       device, [m, n] bf16, row stride n.
+ *  Everything else as for sfp8_sparse_linear and sfp8_sparse_linear_quant.
+ */
+sfp8_status sfp8_prepare_gated_weight_24(const void* w_gate, const void* w_up,
+                                         sfp8_dtype w_dtype, int64_t n, int64_t k,
+                                         int64_t ld_w, sfp8_dtype q_dtype, void* packed,
+                                         float* s_w, void* stream);
+size_t sfp8_gated_linear_workspace_bytes(int64_t m, int64_t n, int64_t k);
+sfp8_status sfp8_gated_linear(const void* a_q, sfp8_dtype a_dtype, const float* s_a,
+                              int64_t m, const void* packed, sfp8_dtype w_dtype,
+                              const float* s_w, int64_t n, int64_t k, sfp8_activation act,
+                              const void* bias, void* h, void* workspace,
+                              size_t workspace_bytes, void* stream);
+size_t sfp8_gated_linear_quant_workspace_bytes(int64_t m, int64_t n, int64_t k);
+sfp8_status sfp8_gated_linear_quant(const void* x, sfp8_dtype x_dtype, int64_t ld_x,
+                                    sfp8_dtype a_dtype, void* a_q, float* s_a, int64_t m,
+                                    const void* packed, sfp8_dtype w_dtype, const float* s_w,
+                                    int64_t n, int64_t k, sfp8_activation act,
+                                    const void* bias, void* h, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /*
  * The layer's forward from host memory to host memory in one call: on

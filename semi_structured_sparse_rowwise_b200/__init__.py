@@ -22,7 +22,9 @@ from .binding import (Sfp8Error, load_library, library_path, new_workspace,
                       sfp8_sparse_linear_quant, sfp8_sparse_linear_quant_workspace_bytes,
                       sfp8_sparse_linear_quant_host, sfp8_sparse_linear_quant_fused,
                       sfp8_sparse_linear_quant_chained, sfp8_sparse_linear_quant_fusable,
-                      new_quant_workspace, sfp8_read_device_status, sfp8_selftest_timeout,
+                      new_quant_workspace, sfp8_prepare_gated_weight_24,
+                      new_gated_workspace, new_gated_quant_workspace, sfp8_gated_linear,
+                      sfp8_gated_linear_quant, sfp8_read_device_status, sfp8_selftest_timeout,
                       sfp8_status_string, sfp8_layout_version)
 from .layer import HostPipeline, SparseFp8Linear
 
@@ -42,6 +44,8 @@ __all__ = [
     "sfp8_sparse_linear_algo", "sfp8_sparse_linear_search", "sfp8_sparse_linear_set_algo",
     "sfp8_sparse_linear_get_algo",
     "sfp8_sparse_linear_quant_workspace_bytes", "new_quant_workspace",
+    "sfp8_prepare_gated_weight_24", "new_gated_workspace", "new_gated_quant_workspace",
+    "sfp8_gated_linear", "sfp8_gated_linear_quant",
     "sfp8_read_device_status", "sfp8_selftest_timeout", "sfp8_status_string",
     "sfp8_layout_version", "SparseFp8Linear", "HostPipeline",
 ]

@@ -26,6 +26,7 @@ STATUS_NAMES = {
 DTYPE = {"bf16": 0, "f16": 1, "f32": 2, "e4m3": 3, "e5m2": 4}
 TORCH_WIDE = {torch.bfloat16: "bf16", torch.float16: "f16", torch.float32: "f32"}
 AMAX_MODE = {"reduce": 0, "atomic": 1}
+ACTIVATION = {"silu": 0, "gelu": 1}
 DEVICE_TIMEOUT = 0x1
 DEVICE_CHECK_FAIL = 0x2
 
@@ -85,6 +86,16 @@ SIGNATURES = {
                                                 _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
                                                 _sz, _c_void_p]),
     "sfp8_sparse_linear_quant_fusable": (_i32, [_i64, _i64, _i64]),
+    "sfp8_prepare_gated_weight_24": (_i32, [_c_void_p, _c_void_p, _i32, _i64, _i64, _i64, _i32,
+                                            _c_void_p, _c_void_p, _c_void_p]),
+    "sfp8_gated_linear_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "sfp8_gated_linear": (_i32, [_c_void_p, _i32, _c_void_p, _i64, _c_void_p, _i32, _c_void_p,
+                                 _i64, _i64, _i32, _c_void_p, _c_void_p, _c_void_p, _sz,
+                                 _c_void_p]),
+    "sfp8_gated_linear_quant_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "sfp8_gated_linear_quant": (_i32, [_c_void_p, _i32, _i64, _i32, _c_void_p, _c_void_p, _i64,
+                                       _c_void_p, _i32, _c_void_p, _i64, _i64, _i32, _c_void_p,
+                                       _c_void_p, _c_void_p, _sz, _c_void_p]),
     "sfp8_selftest_timeout": (_i32, [_c_void_p]),
     "sfp8_sparse_linear_quant_host": (_i32, [_c_void_p, _c_void_p, _i32, _i32, _c_void_p,
                                              _c_void_p, _i64, _c_void_p, _i32, _c_void_p, _i64,
@@ -579,6 +590,151 @@ def _quant_linear(name, x, a_dtype, packed, w_dtype, s_w, n, k, bias, out, works
                                 _ptr(s_w), n, k, _ptr(bias), _ptr(out), _ptr(workspace),
                                 _ws_bytes(workspace, dev), _stream(dev))
     _check(st, name)
+    return out, a_q, s_a
+
+
+# ---------------------------------------------------------------- gated feed-forward block
+
+
+def _activation(act):
+    if act not in ACTIVATION:
+        raise ValueError("act must be 'silu' or 'gelu'")
+    return ACTIVATION[act]
+
+
+def _tensor(t, what, shape, dtype, device):
+    """Refuses anything but a contiguous tensor of this shape, dtype and device."""
+    if (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()
+            or t.device != torch.device(device)):
+        raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
+                         % (what, dtype, tuple(shape), device))
+
+
+def _weight(packed, s_w, rows, k, device):
+    """The compressed weight of `rows` rows and its scales, on `device`."""
+    need = load_library().sfp8_compressed_bytes(rows, k)
+    if (packed.device != device or packed.dtype != torch.uint8 or not packed.is_contiguous()
+            or packed.numel() < need):
+        raise ValueError("packed must be a contiguous uint8 tensor of at least %d bytes on %s"
+                         % (need, device))
+    _tensor(s_w, "s_w", (rows,), torch.float32, device)
+
+
+def _gated_args(n, k, packed, s_w, bias, device):
+    if n < 0:
+        raise ValueError("n must not be negative")
+    _weight(packed, s_w, 2 * n, k, device)
+    if bias is not None:
+        _tensor(bias, "bias", (2 * n,), torch.bfloat16, device)
+
+
+def sfp8_prepare_gated_weight_24(w_gate, w_up, q_dtype="e4m3", packed=None, scales=None):
+    """w_gate, w_up [n, k] bf16/f16/f32 (unit column stride, the same type and
+    strides) -> (packed, s_w): the compressed weight of a gated block, 2n rows
+    that alternate gate and up, each prepared as by sfp8_prepare_weight_24."""
+    lib = load_library()
+    _require_cuda(w_gate, w_up)
+    if w_gate.dim() != 2 or w_gate.stride(1) != 1:
+        raise ValueError("w_gate must be 2-D with unit column stride")
+    if (w_up.shape != w_gate.shape or w_up.dtype != w_gate.dtype or w_up.device != w_gate.device
+            or w_up.stride(1) != 1 or (w_gate.shape[0] > 1 and w_up.stride(0) != w_gate.stride(0))):
+        raise ValueError("w_up must have w_gate's shape, dtype, device and strides")
+    wd = TORCH_WIDE.get(w_gate.dtype)
+    if wd is None:
+        raise ValueError("weight dtype must be bfloat16, float16 or float32")
+    n, k = w_gate.shape
+    if packed is None:
+        packed = torch.empty((lib.sfp8_compressed_bytes(2 * n, k),), dtype=torch.uint8,
+                             device=w_gate.device)
+    if scales is None:
+        scales = torch.empty((2 * n,), dtype=torch.float32, device=w_gate.device)
+    _weight(packed, scales, 2 * n, k, w_gate.device)
+    ld = w_gate.stride(0) if n > 1 else k
+    with torch.cuda.device(w_gate.device):
+        st = lib.sfp8_prepare_gated_weight_24(_ptr(w_gate), _ptr(w_up), DTYPE[wd], n, k, ld,
+                                              DTYPE[_fp8_name(q_dtype)], _ptr(packed),
+                                              _ptr(scales), _stream(w_gate.device))
+    _check(st, "sfp8_prepare_gated_weight_24")
+    return packed, scales
+
+
+def _new_workspace(query, m, n, k, device):
+    with torch.cuda.device(device):
+        nbytes = int(query(m, n, k))
+    return torch.zeros((max(nbytes, 16),), dtype=torch.uint8, device=device)
+
+
+def new_gated_workspace(m, n, k, device):
+    """A zeroed workspace for sfp8_gated_linear(m, n, k) on `device`."""
+    return _new_workspace(load_library().sfp8_gated_linear_workspace_bytes, m, n, k, device)
+
+
+def new_gated_quant_workspace(m, n, k, device):
+    """A zeroed workspace for sfp8_gated_linear_quant(m, n, k) on `device`."""
+    return _new_workspace(load_library().sfp8_gated_linear_quant_workspace_bytes, m, n, k, device)
+
+
+def sfp8_gated_linear(a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k, act="silu", bias=None,
+                      out=None, workspace=None):
+    """h [m, n] bf16 = act(gate) * up of a quantised activation a_q [m, k],
+    s_a [m]; packed, s_w from sfp8_prepare_gated_weight_24, bias [2n] bf16
+    (gate's n values, then up's)."""
+    lib = load_library()
+    _require_cuda(a_q, s_a, packed, s_w, bias)
+    if a_q.dim() != 2:
+        raise ValueError("a_q must be 2-D")
+    m, dev = a_q.shape[0], a_q.device
+    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
+    _tensor(s_a, "s_a", (m,), torch.float32, dev)
+    _gated_args(n, k, packed, s_w, bias, dev)
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+    _tensor(out, "out", (m, n), torch.bfloat16, dev)
+    if workspace is None:
+        workspace = new_gated_workspace(m, n, k, dev)
+    with torch.cuda.device(dev):
+        st = lib.sfp8_gated_linear(_ptr(a_q), DTYPE[_fp8_name(a_dtype)], _ptr(s_a), m,
+                                   _ptr(packed), DTYPE[_fp8_name(w_dtype)], _ptr(s_w), n, k,
+                                   _activation(act), _ptr(bias), _ptr(out), _ptr(workspace),
+                                   _ws_bytes(workspace, dev), _stream(dev))
+    _check(st, "sfp8_gated_linear")
+    return out
+
+
+def sfp8_gated_linear_quant(x, a_dtype, packed, w_dtype, s_w, n, k, act="silu", bias=None,
+                            out=None, workspace=None, a_q=None, s_a=None):
+    """Quantise x [m, k] (bf16/f16/f32, unit column stride) row-wise and apply
+    the gated block, one library call: returns (h [m, n] bf16, a_q [m, k]
+    uint8, s_a [m] f32); a_q and s_a are what the backward pass needs."""
+    lib = load_library()
+    _require_cuda(x, packed, s_w, bias)
+    if x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != k:
+        raise ValueError("x must be [m, k=%d] with unit column stride" % k)
+    m, dev = x.shape[0], x.device
+    xd = TORCH_WIDE.get(x.dtype)
+    if xd is None:
+        raise ValueError("x dtype must be bfloat16, float16 or float32")
+    _gated_args(n, k, packed, s_w, bias, dev)
+    if out is None:
+        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
+    if a_q is None:
+        a_q = torch.empty((m, k), dtype=torch.uint8, device=dev)
+    if s_a is None:
+        s_a = torch.empty((m,), dtype=torch.float32, device=dev)
+    _tensor(out, "out", (m, n), torch.bfloat16, dev)
+    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
+    _tensor(s_a, "s_a", (m,), torch.float32, dev)
+    if workspace is None:
+        workspace = new_gated_quant_workspace(m, n, k, dev)
+    ld = x.stride(0) if m > 1 else k
+    with torch.cuda.device(dev):
+        st = lib.sfp8_gated_linear_quant(_ptr(x), DTYPE[xd], ld, DTYPE[_fp8_name(a_dtype)],
+                                         _ptr(a_q), _ptr(s_a), m, _ptr(packed),
+                                         DTYPE[_fp8_name(w_dtype)], _ptr(s_w), n, k,
+                                         _activation(act), _ptr(bias), _ptr(out),
+                                         _ptr(workspace), _ws_bytes(workspace, dev),
+                                         _stream(dev))
+    _check(st, "sfp8_gated_linear_quant")
     return out, a_q, s_a
 
 

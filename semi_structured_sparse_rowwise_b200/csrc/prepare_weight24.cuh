@@ -144,9 +144,12 @@ __device__ __forceinline__ void prepare_chunk(const uint32_t* in, const uint32_t
 // segment (the amax) and keeps the last one; sweep 2 converts that one from
 // registers and reloads the others (from L2).  A row of one segment (k <= 4096
 // for 16-bit inputs, <= 2048 for fp32) is read from memory once.
+// With w_up (a gated block's pair of weights), row r of the n is row r / 2 of
+// w (r even) or of w_up (r odd).
 template <typename T, int kFmt>
 __global__ void __launch_bounds__(32 * kPrepWarps)
-    prepare_weight24_kernel(const T* __restrict__ w, int64_t n, int64_t k, int64_t ld,
+    prepare_weight24_kernel(const T* __restrict__ w, const T* __restrict__ w_up, int64_t n,
+                            int64_t k, int64_t ld,
                             uint8_t* __restrict__ packed, float* __restrict__ s_w,
                             int64_t n_pad) {
   using Tr = InputTraits<T>;
@@ -178,7 +181,7 @@ __global__ void __launch_bounds__(32 * kPrepWarps)
       }
       continue;
     }
-    const T* wr = w + row * ld;
+    const T* wr = w_up == nullptr ? w + row * ld : ((row & 1) ? w_up : w) + (row >> 1) * ld;
     uint32_t in[kCpl][kChunkWords];
     auto load_segment = [&](int64_t seg) {
 #pragma unroll

@@ -31,8 +31,9 @@ struct DeviceInfo {
   bool is_sm100 = false;
   int index = 0;
   int num_sms = 0;
-  bool smem_attr_set[40] = {};   // (BN, KS, RA, FQ) instantiations
-  int pair_clusters[4] = {};     // co-resident pairs of the pair kernel by (KS, WT) (0: unknown)
+  bool smem_attr_set[80] = {};   // (BN, KS, RA, FQ) instantiations, then the gated ones
+  int pair_clusters[12] = {};    // co-resident pairs of the pair kernel by (KS, WT) and epilogue
+                                 // (0: unknown)
   int tw_blocks[12] = {};        // co-resident CTAs per SM of the tensor-wise quantiser (0: unknown)
   long long l2_bytes = 0;
 };
@@ -572,14 +573,23 @@ LinearPlan make_plan(int dev, int64_t m, int64_t n, int64_t k, int num_sms) {
   return plan_from_choice(m, n, k, num_sms, default_choice(m, n, k, num_sms));
 }
 
-template <int BN, int KS, bool RA, bool FQ = false>
+// The gated block's epilogue in place of the linear's (gated_epilogue.cuh);
+// the call's n then counts the weight's 2 x hidden rows.
+struct GatedCall {
+  int epi;          // kEpiGated or kEpiGatedGrad
+  int act;          // SFP8_ACT_*
+  const void* dh;   // kEpiGatedGrad: [m, hidden] bf16
+  int64_t ld_out;   // row stride of the output
+};
+
+template <int BN, int KS, bool RA, bool FQ = false, int EPI = kEpiLinear>
 sfp8_status launch_linear_cfg(DeviceInfo* dev, const CUtensorMap& ta, const CUtensorMap& ty,
                               const LinearParams& prm, int smem_bytes, cudaStream_t st) {
-  auto kern = sparse_linear_kernel<BN, KS, RA, FQ>;
-  const int slot =
-      FQ ? 32 + (KS == 1 ? 0 : KS == 2 ? 1 : 2)
+  auto kern = sparse_linear_kernel<BN, KS, RA, FQ, EPI>;
+  const int slot = (EPI == kEpiGated ? 40 : 0) +
+      (FQ ? 32 + (KS == 1 ? 0 : KS == 2 ? 1 : 2)
          : ((BN == 16 ? 0 : BN == 32 ? 1 : BN == 64 ? 2 : BN == 128 ? 3 : 4) * 3 +
-            (KS == 1 ? 0 : KS == 2 ? 1 : 2)) * 2 + (RA ? 1 : 0);
+            (KS == 1 ? 0 : KS == 2 ? 1 : 2)) * 2 + (RA ? 1 : 0));
   {
     std::lock_guard<std::mutex> lock(g_mutex);
     if (!dev->smem_attr_set[slot]) {
@@ -648,14 +658,15 @@ sfp8_status encode_act_3d(CUtensorMap* map, const void* base, uint64_t m, uint64
 }
 
 
-// Output map: y [m, n] bf16 row-major, box 128 columns x box_rows rows.
-sfp8_status encode_y_2d(CUtensorMap* map, void* y, uint64_t m, uint64_t n, uint32_t box_rows) {
+// Output map: y [m, n] bf16 row-major, box box_cols columns x box_rows rows.
+sfp8_status encode_y_2d(CUtensorMap* map, void* y, uint64_t m, uint64_t n, uint32_t box_cols,
+                        uint32_t box_rows) {
   EncodeTiledFn enc = nullptr;
   sfp8_status s = get_encoder(&enc);
   if (s != SFP8_OK) return s;
   cuuint64_t dims[2] = {n, m};
   cuuint64_t strides[1] = {n * 2};
-  cuuint32_t box[2] = {static_cast<cuuint32_t>(kTileN), box_rows};
+  cuuint32_t box[2] = {box_cols, box_rows};
   cuuint32_t estr[2] = {1, 1};
   CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, y, dims, strides, box, estr,
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -693,6 +704,7 @@ struct XSpan {
   const void* x;
   sfp8_dtype dtype;
   int64_t ld;
+  int64_t y_cols;
 };
 
 // Validation shared by the sparse-linear entry points (everything except the
@@ -717,7 +729,7 @@ sfp8_status validate_linear(const void* a_q, sfp8_dtype a_dtype, const float* s_
   if (!aligned(a_q, 16) || !aligned(packed, 16) || !aligned(s_a, 4) || !aligned(s_w, 4) ||
       !aligned(y, 2) || (bias != nullptr && !aligned(bias, 2)))
     return SFP8_ERR_MISALIGNED;
-  if (xs != nullptr && outputs_overlap_input(xs->x, xs->dtype, xs->ld, m, k, a_q, s_a, y, n))
+  if (xs != nullptr && outputs_overlap_input(xs->x, xs->dtype, xs->ld, m, k, a_q, s_a, y, xs->y_cols))
     return SFP8_ERR_INVALID_ARG;
   sfp8_status s = current_device(dev);
   if (s != SFP8_OK) return s;
@@ -746,14 +758,14 @@ int pair_band(const DeviceInfo* dev, const LinearPlan& pl, int64_t m, int64_t n,
 
 // CTA-pair GEMM: both maps, the co-resident pair count (queried once per
 // device), launch with programmatic stream serialisation.
-template <int KS, int WT>
+template <int KS, int WT, int EPI>
 sfp8_status launch_pair_cfg(DeviceInfo* dev, const LinearPlan& pl, const void* a_q,
                             sfp8_dtype a_dtype, const float* s_a, int64_t m, const void* packed,
                             sfp8_dtype w_dtype, const float* s_w, int64_t n, int64_t k,
-                            const void* bias, void* y, cudaStream_t st) {
+                            const void* bias, void* y, cudaStream_t st, const GatedCall* gc) {
   using Cfg = PairCfg<KS, WT>;
-  auto kern = sparse_linear_pair_kernel<KS, WT>;
-  constexpr int slot = (KS - 1) * 2 + (WT - 1);
+  auto kern = sparse_linear_pair_kernel<KS, WT, EPI>;
+  constexpr int slot = EPI * 4 + (KS - 1) * 2 + (WT - 1);
   {
     std::lock_guard<std::mutex> lock(g_mutex);
     if (dev->pair_clusters[slot] == 0) {
@@ -817,29 +829,53 @@ sfp8_status launch_pair_cfg(DeviceInfo* dev, const LinearPlan& pl, const void* a
   prm.producers = pl.producers;
   prm.idesc = make_idesc_f8f6f4(w_dtype == SFP8_E5M2 ? 1u : 0u, a_dtype == SFP8_E5M2 ? 1u : 0u,
                                 kPairTileN, static_cast<uint32_t>(pl.bn), true);
+  if (EPI != kEpiLinear) {
+    prm.act = gc->act;
+    prm.dh = static_cast<const __nv_bfloat16*>(gc->dh);
+    prm.ld_out = gc->ld_out;
+  }
   return launch_dependent(kern, dim3(2 * pairs), dim3(Cfg::kThreads), pl.smem_bytes, st, tw2,
                           tw, ta, prm);
+}
+
+template <int EPI>
+sfp8_status launch_pair_epi(DeviceInfo* dev, const LinearPlan& pl, const void* a_q,
+                            sfp8_dtype a_dtype, const float* s_a, int64_t m, const void* packed,
+                            sfp8_dtype w_dtype, const float* s_w, int64_t n, int64_t k,
+                            const void* bias, void* y, cudaStream_t st, const GatedCall* gc) {
+  switch (pl.ks * 2 + pl.wt) {
+    case 1 * 2 + 1:
+      return launch_pair_cfg<1, 1, EPI>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n,
+                                        k, bias, y, st, gc);
+    case 1 * 2 + 2:
+      return launch_pair_cfg<1, 2, EPI>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n,
+                                        k, bias, y, st, gc);
+    case 2 * 2 + 1:
+      return launch_pair_cfg<2, 1, EPI>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n,
+                                        k, bias, y, st, gc);
+    case 2 * 2 + 2:
+      return launch_pair_cfg<2, 2, EPI>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n,
+                                        k, bias, y, st, gc);
+    default:
+      return SFP8_ERR_UNSUPPORTED_SHAPE;   // no such plan is made
+  }
 }
 
 sfp8_status launch_pair(DeviceInfo* dev, const LinearPlan& pl, const void* a_q,
                         sfp8_dtype a_dtype, const float* s_a, int64_t m, const void* packed,
                         sfp8_dtype w_dtype, const float* s_w, int64_t n, int64_t k,
-                        const void* bias, void* y, cudaStream_t st) {
-  switch (pl.ks * 2 + pl.wt) {
-    case 1 * 2 + 1:
-      return launch_pair_cfg<1, 1>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n, k,
-                                   bias, y, st);
-    case 1 * 2 + 2:
-      return launch_pair_cfg<1, 2>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n, k,
-                                   bias, y, st);
-    case 2 * 2 + 1:
-      return launch_pair_cfg<2, 1>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n, k,
-                                   bias, y, st);
-    case 2 * 2 + 2:
-      return launch_pair_cfg<2, 2>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n, k,
-                                   bias, y, st);
+                        const void* bias, void* y, cudaStream_t st,
+                        const GatedCall* gc = nullptr) {
+  switch (gc == nullptr ? static_cast<int>(kEpiLinear) : gc->epi) {
+    case kEpiLinear:
+      return launch_pair_epi<kEpiLinear>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n,
+                                         k, bias, y, st, gc);
+    case kEpiGated:
+      return launch_pair_epi<kEpiGated>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n,
+                                        k, bias, y, st, gc);
     default:
-      return SFP8_ERR_UNSUPPORTED_SHAPE;   // no such plan is made
+      return launch_pair_epi<kEpiGatedGrad>(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w,
+                                            n, k, bias, y, st, gc);
   }
 }
 
@@ -859,16 +895,49 @@ bool fusable(const LinearPlan& pl, int64_t m) {
          m <= kFusedMaxTokens;
 }
 
+// The one-CTA kernel of a plan, without fused quantisation.
+template <int EPI>
+sfp8_status launch_linear_epi(DeviceInfo* dev, const LinearPlan& pl, const CUtensorMap& ta,
+                              const CUtensorMap& ty, const LinearParams& prm, cudaStream_t st) {
+  const int sm = pl.smem_bytes;
+  if (pl.ra) {
+    switch (pl.bn * 8 + pl.ks) {
+      case 16 * 8 + 1: return launch_linear_cfg<16, 1, true, false, EPI>(dev, ta, ty, prm, sm, st);
+      case 16 * 8 + 2: return launch_linear_cfg<16, 2, true, false, EPI>(dev, ta, ty, prm, sm, st);
+      case 16 * 8 + 4: return launch_linear_cfg<16, 4, true, false, EPI>(dev, ta, ty, prm, sm, st);
+      case 32 * 8 + 1: return launch_linear_cfg<32, 1, true, false, EPI>(dev, ta, ty, prm, sm, st);
+      case 32 * 8 + 2: return launch_linear_cfg<32, 2, true, false, EPI>(dev, ta, ty, prm, sm, st);
+      case 32 * 8 + 4: return launch_linear_cfg<32, 4, true, false, EPI>(dev, ta, ty, prm, sm, st);
+      default: return SFP8_ERR_UNSUPPORTED_SHAPE;   // no such plan is made
+    }
+  }
+  switch (pl.bn * 8 + pl.ks) {
+    case 16 * 8 + 1: return launch_linear_cfg<16, 1, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    case 16 * 8 + 2: return launch_linear_cfg<16, 2, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    case 16 * 8 + 4: return launch_linear_cfg<16, 4, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    case 32 * 8 + 1: return launch_linear_cfg<32, 1, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    case 32 * 8 + 2: return launch_linear_cfg<32, 2, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    case 32 * 8 + 4: return launch_linear_cfg<32, 4, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    case 64 * 8 + 1: return launch_linear_cfg<64, 1, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    case 64 * 8 + 2: return launch_linear_cfg<64, 2, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    case 128 * 8 + 1: return launch_linear_cfg<128, 1, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    case 128 * 8 + 2: return launch_linear_cfg<128, 2, false, false, EPI>(dev, ta, ty, prm, sm, st);
+    default: return SFP8_ERR_UNSUPPORTED_SHAPE;   // no such plan is made
+  }
+}
+
 // Encodes the activation map and launches the GEMM for a validated plan
-// (with `fq`, a fusable plan: the GEMM quantises x into a_q itself).
+// (with `fq`, a fusable plan: the GEMM quantises x into a_q itself; with
+// `gc`, the gated epilogue).
 sfp8_status launch_linear(DeviceInfo* dev, const LinearPlan& pl, const void* a_q,
                           sfp8_dtype a_dtype, const float* s_a, int64_t m, const void* packed,
                           sfp8_dtype w_dtype, const float* s_w, int64_t n, int64_t k,
                           const void* bias, void* y, float* partials, unsigned int* counters,
                           cudaStream_t st, const void* a_map = nullptr, int64_t a_map_rows = 0,
-                          const FusedQuant* fq = nullptr) {
+                          const FusedQuant* fq = nullptr, const GatedCall* gc = nullptr) {
   if (pl.pair)
-    return launch_pair(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n, k, bias, y, st);
+    return launch_pair(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n, k, bias, y, st,
+                       gc);
   // The activation map reads a_q's m rows, or a_map_rows rows of a_map (a
   // copy padded to the token tile: whole rows instead of out-of-range fill).
   // A fused launch loads no codes and gets no map.
@@ -911,15 +980,22 @@ sfp8_status launch_linear(DeviceInfo* dev, const LinearPlan& pl, const void* a_q
   // aligned); otherwise plain stores.  The unused map is a copy of ta.
   CUtensorMap ty = ta;
   prm.tma_store = 0;
-  if (pl.ra && pl.whole_tiles && pl.tiles <= pl.grid && n % 8 == 0 && aligned(y, 16) &&
+  const int64_t y_cols = gc != nullptr ? n / 2 : n;
+  if (pl.ra && pl.whole_tiles && pl.tiles <= pl.grid && y_cols % 8 == 0 && aligned(y, 16) &&
       static_cast<long long>(pl.bn) * kTileN * 2 <= pl.ra_bytes) {
-    s = encode_y_2d(&ty, y, static_cast<uint64_t>(m), static_cast<uint64_t>(n),
+    s = encode_y_2d(&ty, y, static_cast<uint64_t>(m), static_cast<uint64_t>(y_cols),
+                    static_cast<uint32_t>(gc != nullptr ? kTileN / 2 : kTileN),
                     static_cast<uint32_t>(pl.bn));
     if (s != SFP8_OK) return s;
     prm.tma_store = 1;
   }
-  const int sm = pl.smem_bytes;
+  if (gc != nullptr) {
+    if (fq != nullptr || gc->epi != kEpiGated) return SFP8_ERR_INVALID_ARG;   // no such call is made
+    prm.act = gc->act;
+    return launch_linear_epi<kEpiGated>(dev, pl, ta, ty, prm, st);
+  }
   if (fq != nullptr) {
+    const int sm = pl.smem_bytes;
     if (!fusable(pl, m)) return SFP8_ERR_UNSUPPORTED_SHAPE;
     prm.x = fq->x;
     prm.ld_x = fq->ld_x;
@@ -934,30 +1010,7 @@ sfp8_status launch_linear(DeviceInfo* dev, const LinearPlan& pl, const void* a_q
       default: return SFP8_ERR_UNSUPPORTED_SHAPE;   // no such plan is made
     }
   }
-  if (pl.ra) {
-    switch (pl.bn * 8 + pl.ks) {
-      case 16 * 8 + 1: return launch_linear_cfg<16, 1, true>(dev, ta, ty, prm, sm, st);
-      case 16 * 8 + 2: return launch_linear_cfg<16, 2, true>(dev, ta, ty, prm, sm, st);
-      case 16 * 8 + 4: return launch_linear_cfg<16, 4, true>(dev, ta, ty, prm, sm, st);
-      case 32 * 8 + 1: return launch_linear_cfg<32, 1, true>(dev, ta, ty, prm, sm, st);
-      case 32 * 8 + 2: return launch_linear_cfg<32, 2, true>(dev, ta, ty, prm, sm, st);
-      case 32 * 8 + 4: return launch_linear_cfg<32, 4, true>(dev, ta, ty, prm, sm, st);
-      default: return SFP8_ERR_UNSUPPORTED_SHAPE;   // no such plan is made
-    }
-  }
-  switch (pl.bn * 8 + pl.ks) {
-    case 16 * 8 + 1: return launch_linear_cfg<16, 1, false>(dev, ta, ty, prm, sm, st);
-    case 16 * 8 + 2: return launch_linear_cfg<16, 2, false>(dev, ta, ty, prm, sm, st);
-    case 16 * 8 + 4: return launch_linear_cfg<16, 4, false>(dev, ta, ty, prm, sm, st);
-    case 32 * 8 + 1: return launch_linear_cfg<32, 1, false>(dev, ta, ty, prm, sm, st);
-    case 32 * 8 + 2: return launch_linear_cfg<32, 2, false>(dev, ta, ty, prm, sm, st);
-    case 32 * 8 + 4: return launch_linear_cfg<32, 4, false>(dev, ta, ty, prm, sm, st);
-    case 64 * 8 + 1: return launch_linear_cfg<64, 1, false>(dev, ta, ty, prm, sm, st);
-    case 64 * 8 + 2: return launch_linear_cfg<64, 2, false>(dev, ta, ty, prm, sm, st);
-    case 128 * 8 + 1: return launch_linear_cfg<128, 1, false>(dev, ta, ty, prm, sm, st);
-    case 128 * 8 + 2: return launch_linear_cfg<128, 2, false>(dev, ta, ty, prm, sm, st);
-    default: return SFP8_ERR_UNSUPPORTED_SHAPE;   // no such plan is made
-  }
+  return launch_linear_epi<kEpiLinear>(dev, pl, ta, ty, prm, st);
 }
 
 // Workspace of the one-call forward: the GEMM's split-K scratch, then --
@@ -1165,8 +1218,9 @@ sfp8_status sfp8_compress_24(const void* w_q, sfp8_dtype w_dtype, int64_t n, int
 extern "C++" {
 namespace {
 
+// w_up: the second weight of a gated pair (n then counts both), or null.
 template <typename T>
-sfp8_status launch_prepare(const void* w, int64_t n, int64_t k, int64_t ld, sfp8_dtype q_dtype,
+sfp8_status launch_prepare(const void* w, const void* w_up, int64_t n, int64_t k, int64_t ld, sfp8_dtype q_dtype,
                            void* packed, float* s_w, int sms, cudaStream_t st) {
   const int64_t n_pad = sfp8_padded_rows(n);
   auto kernel = q_dtype == SFP8_E4M3 ? prepare_weight24_kernel<T, SFP8_E4M3>
@@ -1184,25 +1238,30 @@ sfp8_status launch_prepare(const void* w, int64_t n, int64_t k, int64_t ld, sfp8
     blocks = std::min<int64_t>(blocks, std::max<int64_t>(sms, (48ll << 20) / (row_bytes * kPrepWarps)));
   blocks = std::min<int64_t>(blocks, n_pad / kPrepWarps);
   kernel<<<static_cast<unsigned>(blocks), 32 * kPrepWarps, 0, st>>>(
-      static_cast<const T*>(w), n, k, ld, static_cast<uint8_t*>(packed), s_w, n_pad);
+      static_cast<const T*>(w), static_cast<const T*>(w_up), n, k, ld,
+      static_cast<uint8_t*>(packed), s_w, n_pad);
   return launch_status();
 }
 
 }  // namespace
 }  // extern "C++"
 
-sfp8_status sfp8_prepare_weight_24(const void* w, sfp8_dtype w_dtype, int64_t n, int64_t k,
-                                   int64_t ld_w, sfp8_dtype q_dtype, void* packed, float* s_w,
-                                   void* stream) {
+// Shared by the one-weight and the gated preparation: n rows in all, w_up
+// null or the second weight of n / 2 rows.
+static sfp8_status prepare_weight(const void* w, const void* w_up, bool gated,
+                                  sfp8_dtype w_dtype, int64_t n, int64_t k, int64_t ld_w,
+                                  sfp8_dtype q_dtype, void* packed, float* s_w, void* stream) {
   if (!is_fp8(q_dtype)) return SFP8_ERR_UNSUPPORTED_DTYPE;
   if (w_dtype != SFP8_BF16 && w_dtype != SFP8_F16 && w_dtype != SFP8_F32)
     return SFP8_ERR_UNSUPPORTED_DTYPE;
   if (n < 0 || k < 0 || ld_w < k) return SFP8_ERR_INVALID_ARG;
   if (k % kStepK != 0 || k == 0) return SFP8_ERR_UNSUPPORTED_SHAPE;
   if (n == 0) return SFP8_OK;
-  if (w == nullptr || packed == nullptr || s_w == nullptr) return SFP8_ERR_INVALID_ARG;
+  if (w == nullptr || packed == nullptr || s_w == nullptr || (gated && w_up == nullptr))
+    return SFP8_ERR_INVALID_ARG;
   const int64_t esize = w_dtype == SFP8_F32 ? 4 : 2;
-  if (!aligned(w, 16) || (ld_w * esize) % 16 != 0 || !aligned(packed, 16) || !aligned(s_w, 4))
+  if (!aligned(w, 16) || (ld_w * esize) % 16 != 0 || !aligned(packed, 16) || !aligned(s_w, 4) ||
+      !aligned(w_up, 16))
     return SFP8_ERR_MISALIGNED;
   DeviceInfo* dev = nullptr;
   sfp8_status s = current_device(&dev);
@@ -1210,12 +1269,19 @@ sfp8_status sfp8_prepare_weight_24(const void* w, sfp8_dtype w_dtype, int64_t n,
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (w_dtype) {
     case SFP8_BF16:
-      return launch_prepare<__nv_bfloat16>(w, n, k, ld_w, q_dtype, packed, s_w, dev->num_sms, st);
+      return launch_prepare<__nv_bfloat16>(w, w_up, n, k, ld_w, q_dtype, packed, s_w,
+                                           dev->num_sms, st);
     case SFP8_F16:
-      return launch_prepare<__half>(w, n, k, ld_w, q_dtype, packed, s_w, dev->num_sms, st);
+      return launch_prepare<__half>(w, w_up, n, k, ld_w, q_dtype, packed, s_w, dev->num_sms, st);
     default:
-      return launch_prepare<float>(w, n, k, ld_w, q_dtype, packed, s_w, dev->num_sms, st);
+      return launch_prepare<float>(w, w_up, n, k, ld_w, q_dtype, packed, s_w, dev->num_sms, st);
   }
+}
+
+sfp8_status sfp8_prepare_weight_24(const void* w, sfp8_dtype w_dtype, int64_t n, int64_t k,
+                                   int64_t ld_w, sfp8_dtype q_dtype, void* packed, float* s_w,
+                                   void* stream) {
+  return prepare_weight(w, nullptr, false, w_dtype, n, k, ld_w, q_dtype, packed, s_w, stream);
 }
 
 sfp8_status sfp8_decompress_24(const void* packed, int64_t n, int64_t k, void* w_q,
@@ -1521,13 +1587,14 @@ static sfp8_status quant_linear(const void* x, sfp8_dtype x_dtype, int64_t ld_x,
                          void* a_q, float* s_a, int64_t m, const void* packed,
                          sfp8_dtype w_dtype, const float* s_w, int64_t n, int64_t k,
                          const void* bias, void* y, void* workspace, size_t workspace_bytes,
-                         void* stream, QuantMode mode) {
+                         void* stream, QuantMode mode, const GatedCall* gc = nullptr) {
   if (!is_wide(x_dtype)) return SFP8_ERR_UNSUPPORTED_DTYPE;
   if (ld_x < k) return SFP8_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;
   LinearPlan pl{};
   bool empty = false;
-  const XSpan xs{x, x_dtype, ld_x};
+  // a gated call's output has half as many columns as the weight has rows
+  const XSpan xs{x, x_dtype, ld_x, gc != nullptr ? n / 2 : n};
   sfp8_status s = validate_linear(a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n, k, bias, y,
                                   &dev, &pl, &empty, &xs);
   if (s != SFP8_OK) return s;
@@ -1542,7 +1609,8 @@ static sfp8_status quant_linear(const void* x, sfp8_dtype x_dtype, int64_t ld_x,
   }
   const bool can_fuse = fusable(pl, m);
   if (mode == kQuantFused && !can_fuse) return SFP8_ERR_UNSUPPORTED_SHAPE;
-  const bool fuse = mode == kQuantFused || (mode == kQuantAuto && can_fuse && kFuseWhenPossible);
+  const bool fuse = gc == nullptr &&
+                    (mode == kQuantFused || (mode == kQuantAuto && can_fuse && kFuseWhenPossible));
   bool pad = false;
   size_t pad_off = 0;
   size_t need = quant_workspace_need(pl, m, k, &pad, &pad_off);
@@ -1566,7 +1634,7 @@ static sfp8_status quant_linear(const void* x, sfp8_dtype x_dtype, int64_t ld_x,
   s = quantize_rowwise_impl(x, x_dtype, m, k, ld_x, a_q, a_dtype, s_a, stream, staged);
   if (s != SFP8_OK) return s;
   return launch_linear(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, n, k, bias, y,
-                       partials, counters, st, staged, pad ? pl.bn : 0);
+                       partials, counters, st, staged, pad ? pl.bn : 0, nullptr, gc);
 }
 
 sfp8_status sfp8_sparse_linear_quant(const void* x, sfp8_dtype x_dtype, int64_t ld_x,
@@ -1606,6 +1674,78 @@ int sfp8_sparse_linear_quant_fusable(int64_t m, int64_t n, int64_t k) {
     return 0;
   const LinearPlan pl = make_plan(dev, m, n, k, sms);
   return fusable(pl, m) ? 1 : 0;
+}
+
+// ---- gated feed-forward block
+
+// The weight rows of a gated block of n hidden units (0 where 2 n is out of
+// range: then nothing below accepts it).
+static int64_t gated_rows(int64_t n) {
+  return n > 0 && n < (int64_t(1) << 30) ? 2 * n : 0;
+}
+
+static bool is_activation(int act) { return act == SFP8_ACT_SILU || act == SFP8_ACT_GELU; }
+
+// What every gated entry point checks before the linear's own validation.
+static sfp8_status validate_gated(int64_t n, int act) {
+  if (!is_activation(act) || n < 0) return SFP8_ERR_INVALID_ARG;
+  if (n >= (int64_t(1) << 30)) return SFP8_ERR_UNSUPPORTED_SHAPE;
+  return SFP8_OK;
+}
+
+sfp8_status sfp8_prepare_gated_weight_24(const void* w_gate, const void* w_up,
+                                         sfp8_dtype w_dtype, int64_t n, int64_t k, int64_t ld_w,
+                                         sfp8_dtype q_dtype, void* packed, float* s_w,
+                                         void* stream) {
+  const sfp8_status s = validate_gated(n, SFP8_ACT_SILU);
+  if (s != SFP8_OK) return s;
+  return prepare_weight(w_gate, w_up, true, w_dtype, 2 * n, k, ld_w, q_dtype, packed, s_w,
+                        stream);
+}
+
+size_t sfp8_gated_linear_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  return sfp8_sparse_linear_workspace_bytes(m, gated_rows(n), k);
+}
+
+sfp8_status sfp8_gated_linear(const void* a_q, sfp8_dtype a_dtype, const float* s_a, int64_t m,
+                              const void* packed, sfp8_dtype w_dtype, const float* s_w,
+                              int64_t n, int64_t k, sfp8_activation act, const void* bias,
+                              void* h, void* workspace, size_t workspace_bytes, void* stream) {
+  sfp8_status s = validate_gated(n, act);
+  if (s != SFP8_OK) return s;
+  DeviceInfo* dev = nullptr;
+  LinearPlan pl{};
+  bool empty = false;
+  s = validate_linear(a_q, a_dtype, s_a, m, packed, w_dtype, s_w, 2 * n, k, bias, h, &dev, &pl,
+                      &empty);
+  if (s != SFP8_OK || empty) return s;
+  const size_t need = pl.partial_bytes + pl.counter_bytes;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SFP8_ERR_WORKSPACE;
+  if (workspace != nullptr && !aligned(workspace, 16)) return SFP8_ERR_MISALIGNED;
+  unsigned int* counters = need > 0 ? reinterpret_cast<unsigned int*>(
+                                          static_cast<uint8_t*>(workspace) + pl.partial_bytes)
+                                    : nullptr;
+  const GatedCall gc{kEpiGated, act, nullptr, n};
+  return launch_linear(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, 2 * n, k, bias, h,
+                       static_cast<float*>(workspace), counters,
+                       static_cast<cudaStream_t>(stream), nullptr, 0, nullptr, &gc);
+}
+
+size_t sfp8_gated_linear_quant_workspace_bytes(int64_t m, int64_t n, int64_t k) {
+  return sfp8_sparse_linear_quant_workspace_bytes(m, gated_rows(n), k);
+}
+
+sfp8_status sfp8_gated_linear_quant(const void* x, sfp8_dtype x_dtype, int64_t ld_x,
+                                    sfp8_dtype a_dtype, void* a_q, float* s_a, int64_t m,
+                                    const void* packed, sfp8_dtype w_dtype, const float* s_w,
+                                    int64_t n, int64_t k, sfp8_activation act, const void* bias,
+                                    void* h, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  const sfp8_status s = validate_gated(n, act);
+  if (s != SFP8_OK) return s;
+  const GatedCall gc{kEpiGated, act, nullptr, n};
+  return quant_linear(x, x_dtype, ld_x, a_dtype, a_q, s_a, m, packed, w_dtype, s_w, 2 * n, k,
+                      bias, h, workspace, workspace_bytes, stream, kQuantChained, &gc);
 }
 
 sfp8_status sfp8_selftest_timeout(void* stream) {

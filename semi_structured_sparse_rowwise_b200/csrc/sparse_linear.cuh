@@ -54,6 +54,10 @@
 // the MMA warp waits for the codes.  The codes and scales also go to global
 // memory, each k step of the codes written by one CTA.
 //
+// Gated form (EPI = kEpiGated, gated_epilogue.cuh): the weight's rows
+// alternate gate and up, and the epilogue stores act(gate) * up, half as many
+// columns as the weight has rows.
+//
 // Every wait is bounded (device_common.cuh): on a timeout the CTA records
 // SFP8_DEVICE_TIMEOUT, lets its copies in flight land, drains its MMAs,
 // frees its tensor memory and returns.
@@ -62,6 +66,7 @@
 #include <cuda_bf16.h>
 
 #include "device_common.cuh"
+#include "gated_epilogue.cuh"
 #include "quantize_rowwise.cuh"
 
 namespace sfp8 {
@@ -142,6 +147,8 @@ struct LinearParams {
   int a_fmt;                // SFP8_E4M3 / SFP8_E5M2
   uint8_t* a_q_out;         // codes [m][k], written (k step t by CTA t mod grid)
   float* s_a_out;           // row scales [m], written by CTA 0
+  // gated form only: n counts the 2 x hidden rows, y is [m][n / 2]
+  int act;                  // SFP8_ACT_*
 };
 
 // The work of one CTA, one tile segment [u0, u1) (in stages) at a time.  All
@@ -196,10 +203,27 @@ __device__ __forceinline__ const float* partial_slot(const LinearParams& p, int 
   return p.partials + (static_cast<long long>(cc) * 2 + slot) * (BN * kTileN);
 }
 
-// Epilogue of one 16-column chunk: y = acc * (s_a * s_w) + bias.
+// Epilogue of one 16-column chunk: y = acc * (s_a * s_w) + bias, or in the
+// gated form the product h of neighbouring rows (see gated_epilogue.cuh).
+template <int EPI>
 __device__ __forceinline__ void store_chunk(const LinearParams& p, const float (&acc)[16],
                                             const float (&sa)[16], int n, int m0, float sw,
                                             float bias) {
+  if constexpr (EPI == kEpiGated) {
+    float z[16], g[8], u[8];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) z[j] = fmaf(acc[j], sa[j] * sw, bias);
+    gated_pair_up(z, n & 1, g, u);
+    if (n >= p.n) return;
+    const int first = m0 + (n & 1) * 8;
+    const int width = p.n >> 1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (first + j < p.m)
+        p.y[static_cast<long long>(first + j) * width + (n >> 1)] =
+            __float2bfloat16_rn(act_value(g[j], p.act) * u[j]);
+    return;
+  }
   if (n >= p.n) return;
 #pragma unroll
   for (int j = 0; j < 16; ++j) {
@@ -331,11 +355,12 @@ __device__ __forceinline__ void fused_quantize_all(const LinearParams& p, int qt
   if (qt == 0) mbar_arrive(smem_u32(ra_bar));
 }
 
-template <int BN, int KS, bool RA, bool FQ = false>
+template <int BN, int KS, bool RA, bool FQ = false, int EPI = kEpiLinear>
 __global__ void __launch_bounds__(linear_threads(FQ), 1)
     sparse_linear_kernel(const __grid_constant__ CUtensorMap tm_a,
                          const __grid_constant__ CUtensorMap tm_y, const LinearParams p) {
   static_assert(!FQ || (RA && BN == kFusedMaxTokens), "fused quantisation: one 16-token tile");
+  static_assert(EPI == kEpiLinear || EPI == kEpiGated, "epilogues of this kernel");
   using Cfg = LinearCfg<BN, KS, RA>;
   const int S = p.stages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -611,7 +636,8 @@ __global__ void __launch_bounds__(linear_threads(FQ), 1)
       // Everything the epilogue needs besides the accumulator, loaded before
       // waiting for it.
       const float sw = (n < p.n) ? __ldg(p.s_w + n) : 0.0f;
-      const float bv = (p.bias != nullptr && n < p.n) ? __bfloat162float(p.bias[n]) : 0.0f;
+      const long long bias_at = EPI == kEpiGated ? gated_bias_index(n, p.n) : n;
+      const float bv = (p.bias != nullptr && n < p.n) ? __bfloat162float(p.bias[bias_at]) : 0.0f;
       float sa0[16];
       load_sa<FQ>(p, mt * BN, sa0, sa_sm);
       int c_first = cta, c_last = cta;
@@ -656,12 +682,26 @@ __global__ void __launch_bounds__(linear_threads(FQ), 1)
         if (whole && p.tma_store) {
           // stage the bf16 tile [BN tokens][128 rows] in the resident
           // activation's region, free once the tile's MMAs have completed
+          // (gated: [BN tokens][64 hidden units])
           __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(ra_base);
+          if constexpr (EPI == kEpiGated) {
+            float z[16], g[8], u2[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j)
-            stg[(c * 16 + j) * kTileN + n_local] = __float2bfloat16_rn(fmaf(v[j], sa[j] * sw, bv));
+            for (int j = 0; j < 16; ++j) z[j] = fmaf(v[j], sa[j] * sw, bv);
+            gated_pair_up(z, n_local & 1, g, u2);
+            const int first = c * 16 + (n_local & 1) * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              stg[(first + j) * (kTileN / 2) + n_local / 2] =
+                  __float2bfloat16_rn(act_value(g[j], p.act) * u2[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+              stg[(c * 16 + j) * kTileN + n_local] =
+                  __float2bfloat16_rn(fmaf(v[j], sa[j] * sw, bv));
+          }
         } else if (whole) {
-          store_chunk(p, v, sa, n, mt * BN + c * 16, sw, bv);
+          store_chunk<EPI>(p, v, sa, n, mt * BN + c * 16, sw, bv);
         } else if (finish_now) {
           float sum[16];
 #pragma unroll
@@ -679,7 +719,7 @@ __global__ void __launch_bounds__(linear_threads(FQ), 1)
               for (int j = 0; j < 16; ++j) sum[j] += a[j];
             }
           }
-          store_chunk(p, sum, sa, n, mt * BN + c * 16, sw, bv);
+          store_chunk<EPI>(p, sum, sa, n, mt * BN + c * 16, sw, bv);
         } else {
 #pragma unroll
           for (int j = 0; j < 16; ++j) part[(c * 16 + j) * kTileN + n_local] = v[j];
@@ -691,7 +731,8 @@ __global__ void __launch_bounds__(linear_threads(FQ), 1)
         fence_proxy_async_smem();
         named_barrier_sync(1, kEpiThreads);
         if (warp == kEpiWarp0 && lane == 0) {
-          tma_store_2d(&tm_y, smem_u32(ra_base), nt * kTileN, mt * BN);
+          tma_store_2d(&tm_y, smem_u32(ra_base),
+                       EPI == kEpiGated ? nt * (kTileN / 2) : nt * kTileN, mt * BN);
           bulk_commit_group();
           bulk_wait_group_0();
         }
@@ -744,7 +785,7 @@ __global__ void __launch_bounds__(linear_threads(FQ), 1)
 #pragma unroll
               for (int j = 0; j < 16; ++j) v[j] += __ldcg(s0 + j * kTileN);
             }
-            store_chunk(p, v, sa, n, mt * BN + c * 16, sw, bv);
+            store_chunk<EPI>(p, v, sa, n, mt * BN + c * 16, sw, bv);
           }
           if (lane == 0) *counter = 0u;
         }

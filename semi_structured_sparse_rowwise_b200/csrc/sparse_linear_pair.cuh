@@ -40,6 +40,11 @@
 // (pair_tile_coords), pair p takes tiles p, p + pairs, ...  No split-K.  Tensor memory: accumulator b at columns
 // [224 b, 224 b + BN), metadata of the stage's k steps at 448.
 //
+// Gated forms (gated_epilogue.cuh), over a weight whose rows alternate gate
+// and up: EPI = kEpiGated stores act(gate) * up; EPI = kEpiGatedGrad, the
+// first step of the block's backward pass, computes gate and up again from
+// the forward's 8-bit activation and stores the gradient of both from dh.
+//
 // Every wait is bounded (device_common.cuh); a timed-out CTA records
 // SFP8_DEVICE_TIMEOUT and runs to the final cluster barrier, which both CTAs
 // always reach.
@@ -102,6 +107,10 @@ struct PairParams {
   int stage_bytes;  // PairCfg<KS>::stage_bytes(bn)
   int producers;
   uint32_t idesc;
+  // gated forms only: n counts the 2 x hidden rows
+  int act;                  // SFP8_ACT_*
+  const __nv_bfloat16* dh;  // [m][n / 2] (kEpiGatedGrad)
+  long long ld_out;         // row stride of y: h's n / 2, dz's padded width
 };
 
 // Tile t -> (weight group g, token tile mt).  Tiles run in bands of p.band
@@ -126,7 +135,7 @@ __device__ __forceinline__ void load_sa_pair(const PairParams& p, int m0, float 
   for (int j = 0; j < 16; ++j) sa[j] = (m0 + j < p.m) ? __ldg(p.s_a + m0 + j) : 0.0f;
 }
 
-template <int KS, int WT>
+template <int KS, int WT, int EPI = kEpiLinear>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kThreads, 1)
     sparse_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w2,
                               const __grid_constant__ CUtensorMap tm_w,
@@ -356,7 +365,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
       const int nt = 2 * WT * g + WT * static_cast<int>(rank) + slot;
       const int n = nt * kTileN + q * 32 + lane;
       const float sw = (n < p.n) ? __ldg(p.s_w + n) : 0.0f;
-      const float bv = (p.bias != nullptr && n < p.n) ? __bfloat162float(p.bias[n]) : 0.0f;
+      const long long bias_at = EPI != kEpiLinear ? gated_bias_index(n, p.n) : n;
+      const float bv = (p.bias != nullptr && n < p.n) ? __bfloat162float(p.bias[bias_at]) : 0.0f;
       int ok = 1;
       if (lane == 0) ok = mbar_wait(smem_u32(&accf_bar[acc]), acc_phase, abort_flag) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -371,14 +381,48 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
         tmem_ld_32x32b_x16(t_row + c * 16, r);
         float sa[16];
         load_sa_pair(p, m_tile0 + c * 16, sa);
-        tmem_ld_wait();
-        if (n < p.n) {
+        if constexpr (EPI == kEpiLinear) {
+          tmem_ld_wait();
+          if (n < p.n) {
 #pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int m = m_tile0 + c * 16 + j;
-            if (m < p.m)
-              p.y[static_cast<long long>(m) * p.n + n] =
-                  __float2bfloat16_rn(fmaf(__uint_as_float(r[j]), sa[j] * sw, bv));
+            for (int j = 0; j < 16; ++j) {
+              const int m = m_tile0 + c * 16 + j;
+              if (m < p.m)
+                p.y[static_cast<long long>(m) * p.n + n] =
+                    __float2bfloat16_rn(fmaf(__uint_as_float(r[j]), sa[j] * sw, bv));
+            }
+          }
+        } else {
+          const int first = m_tile0 + c * 16 + (n & 1) * 8;   // this lane's eight tokens
+          float dh[8];
+          if constexpr (EPI == kEpiGatedGrad) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              dh[j] = (n < p.n && first + j < p.m)
+                          ? __bfloat162float(
+                                p.dh[static_cast<long long>(first + j) * (p.n >> 1) + (n >> 1)])
+                          : 0.0f;
+          }
+          tmem_ld_wait();
+          float z[16], g[8], u[8];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) z[j] = fmaf(__uint_as_float(r[j]), sa[j] * sw, bv);
+          gated_pair_up(z, n & 1, g, u);
+          if (n < p.n) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (first + j >= p.m) continue;
+              __nv_bfloat16* row = p.y + static_cast<long long>(first + j) * p.ld_out;
+              if constexpr (EPI == kEpiGated) {
+                row[n >> 1] = __float2bfloat16_rn(act_value(g[j], p.act) * u[j]);
+              } else {
+                float f, df;
+                act_value_grad(g[j], p.act, f, df);
+                // gate's and up's gradient, neighbours in dz
+                *reinterpret_cast<__nv_bfloat162*>(row + (n & ~1)) =
+                    __floats2bfloat162_rn(dh[j] * u[j] * df, dh[j] * f);
+              }
+            }
           }
         }
       }
