@@ -508,6 +508,59 @@ sfp8_status sfp8_gated_linear_quant(const void* x, sfp8_dtype x_dtype, int64_t l
                                     size_t workspace_bytes, void* stream);
 
 /*
+ * Backward passes from 8-bit activation checkpoints.  A forward call leaves
+ * its quantised activation a_q, s_a with the caller; keeping those (1 byte
+ * per element and 4 per row) is all that the backward pass needs of x, and
+ * the gated block's gate and up are computed again from them.  Both
+ * quantisers are passed straight through (their derivative is taken as 1), and
+ * the weight's gradient is dense, dropped slots included: it is the gradient
+ * for the weight that sfp8_prepare_weight_24 was given.
+ *
+ * sfp8_sparse_linear_backward, from dy [m, n]:
+ *     dx[m, k]  = sum_n dy[m, n] * s_w[n] * W_q[n, k]
+ *     dw[n, k]  = sum_m dy[m, n] * s_a[m] * A_q[m, k]
+ *     dbias[n]  = sum_m dy[m, n]
+ * sfp8_gated_linear_backward, from dh [m, n], first
+ *     dgate = dh * up * act'(gate),   dup = dh * act(gate)
+ * and then the three sums over the 2n rows.
+ * Sums are held in fp32 and the results rounded once to bf16.  The operands
+ * s_w W_q, s_a A_q and dgate, dup enter the tensor cores as bf16, one
+ * rounding (2^-9) each.
+ *
+ *  dy, dh  device, bf16, row stride ld >= n.  dh: any 2-byte aligned.  dy:
+ *          16-byte aligned with ld_dy % 8 == 0, or any if n % 8 != 0 (it is
+ *          then copied to the workspace first).
+ *  a_q, s_a, packed, s_w and dtypes: as in the forward call.  The plain
+ *          linear reads a_q, s_a only for dw and packed, s_w only for dx (they
+ *          may be NULL otherwise).
+ *  n       as in the forward call (gated: hidden units, packed has 2n rows);
+ *  act, bias  as in the gated forward.
+ *  dx      device, [m, k] bf16, 16-byte aligned; or NULL: not computed.
+ *  dw      device, bf16, 16-byte aligned, [n, k]; gated [2n, k]: the n rows of
+ *          gate, then those of up; or NULL.
+ *  dbias   device, bf16, [n]; gated [2n], gate then up; or NULL.
+ *  workspace  16-byte aligned, >= the matching workspace_bytes(m, n, k);
+ *          needs no clearing.  Calls that share one must not overlap.
+ *  k % 128 == 0, k > 0.  m == 0 or n == 0: the outputs asked for are zeros.
+ * Outputs must not overlap each other, the inputs or the workspace.
+ */
+size_t sfp8_sparse_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k);
+sfp8_status sfp8_sparse_linear_backward(const void* dy, int64_t ld_dy, const void* a_q,
+                                        sfp8_dtype a_dtype, const float* s_a, int64_t m,
+                                        const void* packed, sfp8_dtype w_dtype,
+                                        const float* s_w, int64_t n, int64_t k, void* dx,
+                                        void* dw, void* dbias, void* workspace,
+                                        size_t workspace_bytes, void* stream);
+size_t sfp8_gated_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k);
+sfp8_status sfp8_gated_linear_backward(const void* dh, int64_t ld_dh, const void* a_q,
+                                       sfp8_dtype a_dtype, const float* s_a, int64_t m,
+                                       const void* packed, sfp8_dtype w_dtype,
+                                       const float* s_w, int64_t n, int64_t k,
+                                       sfp8_activation act, const void* bias, void* dx,
+                                       void* dw, void* dbias, void* workspace,
+                                       size_t workspace_bytes, void* stream);
+
+/*
  * The layer's forward from host memory to host memory in one call: on
  * `stream`, the copy of x_host into the device staging buffer x_dev, then
  * exactly sfp8_sparse_linear_quant on it, then the copy of y_dev into y_host.

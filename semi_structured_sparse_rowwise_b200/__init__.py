@@ -24,7 +24,9 @@ from .binding import (Sfp8Error, load_library, library_path, new_workspace,
                       sfp8_sparse_linear_quant_chained, sfp8_sparse_linear_quant_fusable,
                       new_quant_workspace, sfp8_prepare_gated_weight_24,
                       new_gated_workspace, new_gated_quant_workspace, sfp8_gated_linear,
-                      sfp8_gated_linear_quant, sfp8_read_device_status, sfp8_selftest_timeout,
+                      sfp8_gated_linear_quant, new_linear_backward_workspace,
+                      new_gated_backward_workspace, sfp8_sparse_linear_backward,
+                      sfp8_gated_linear_backward, sfp8_read_device_status, sfp8_selftest_timeout,
                       sfp8_status_string, sfp8_layout_version)
 from .layer import HostPipeline, SparseFp8Linear
 
@@ -45,7 +47,8 @@ __all__ = [
     "sfp8_sparse_linear_get_algo",
     "sfp8_sparse_linear_quant_workspace_bytes", "new_quant_workspace",
     "sfp8_prepare_gated_weight_24", "new_gated_workspace", "new_gated_quant_workspace",
-    "sfp8_gated_linear", "sfp8_gated_linear_quant",
+    "sfp8_gated_linear", "sfp8_gated_linear_quant", "new_linear_backward_workspace",
+    "new_gated_backward_workspace", "sfp8_sparse_linear_backward", "sfp8_gated_linear_backward",
     "sfp8_read_device_status", "sfp8_selftest_timeout", "sfp8_status_string",
     "sfp8_layout_version", "SparseFp8Linear", "HostPipeline",
 ]

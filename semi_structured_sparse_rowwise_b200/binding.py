@@ -96,6 +96,15 @@ SIGNATURES = {
     "sfp8_gated_linear_quant": (_i32, [_c_void_p, _i32, _i64, _i32, _c_void_p, _c_void_p, _i64,
                                        _c_void_p, _i32, _c_void_p, _i64, _i64, _i32, _c_void_p,
                                        _c_void_p, _c_void_p, _sz, _c_void_p]),
+    "sfp8_sparse_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "sfp8_sparse_linear_backward": (_i32, [_c_void_p, _i64, _c_void_p, _i32, _c_void_p, _i64,
+                                           _c_void_p, _i32, _c_void_p, _i64, _i64, _c_void_p,
+                                           _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p]),
+    "sfp8_gated_linear_backward_workspace_bytes": (_sz, [_i64, _i64, _i64]),
+    "sfp8_gated_linear_backward": (_i32, [_c_void_p, _i64, _c_void_p, _i32, _c_void_p, _i64,
+                                          _c_void_p, _i32, _c_void_p, _i64, _i64, _i32,
+                                          _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                          _sz, _c_void_p]),
     "sfp8_selftest_timeout": (_i32, [_c_void_p]),
     "sfp8_sparse_linear_quant_host": (_i32, [_c_void_p, _c_void_p, _i32, _i32, _c_void_p,
                                              _c_void_p, _i64, _c_void_p, _i32, _c_void_p, _i64,
@@ -736,6 +745,99 @@ def sfp8_gated_linear_quant(x, a_dtype, packed, w_dtype, s_w, n, k, act="silu", 
                                          _stream(dev))
     _check(st, "sfp8_gated_linear_quant")
     return out, a_q, s_a
+
+
+# ---------------------------------------------------------------- backward passes
+
+
+def new_linear_backward_workspace(m, n, k, device):
+    """A workspace for sfp8_sparse_linear_backward(m, n, k) on `device`."""
+    return _new_workspace(load_library().sfp8_sparse_linear_backward_workspace_bytes, m, n, k,
+                          device)
+
+
+def new_gated_backward_workspace(m, n, k, device):
+    """A workspace for sfp8_gated_linear_backward(m, n, k) on `device`."""
+    return _new_workspace(load_library().sfp8_gated_linear_backward_workspace_bytes, m, n, k,
+                          device)
+
+
+def _grad_outputs(m, rows, k, need, given, device):
+    """The gradient tensors asked for: a given one (checked), a new one, or None."""
+    out = []
+    for wanted, t, what, shape in zip(need, given, ("dx", "dw", "dbias"),
+                                      ((m, k), (rows, k), (rows,))):
+        if t is not None:
+            _tensor(t, what, shape, torch.bfloat16, device)
+        elif wanted:
+            t = torch.empty(shape, dtype=torch.bfloat16, device=device)
+        out.append(t)
+    return out
+
+
+def _grad_input(dy, what, m, n, device):
+    if (dy.dim() != 2 or tuple(dy.shape) != (m, n) or dy.dtype != torch.bfloat16
+            or dy.device != device or (n > 1 and dy.stride(1) != 1)):
+        raise ValueError("%s must be a bfloat16 tensor of shape %s with unit column stride on %s"
+                         % (what, (m, n), device))
+    return dy.stride(0) if m > 1 else n
+
+
+def sfp8_sparse_linear_backward(dy, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k, need_dx=True,
+                                need_dw=True, need_dbias=False, dx=None, dw=None, dbias=None,
+                                workspace=None):
+    """Gradients of the sparse linear from dy [m, n] bf16 and the forward's
+    8-bit checkpoint a_q [m, k], s_a [m]: returns (dx [m, k], dw [n, k],
+    dbias [n]), bf16, None where not asked for.  A given dx, dw or dbias is
+    written (and counts as asked for)."""
+    lib = load_library()
+    _require_cuda(dy, a_q, s_a, packed, s_w)
+    if a_q.dim() != 2:
+        raise ValueError("a_q must be 2-D")
+    m, dev = a_q.shape[0], a_q.device
+    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
+    _tensor(s_a, "s_a", (m,), torch.float32, dev)
+    _weight(packed, s_w, n, k, dev)
+    ld = _grad_input(dy, "dy", m, n, dev)
+    dx, dw, dbias = _grad_outputs(m, n, k, (need_dx, need_dw, need_dbias), (dx, dw, dbias), dev)
+    if workspace is None:
+        workspace = new_linear_backward_workspace(m, n, k, dev)
+    with torch.cuda.device(dev):
+        st = lib.sfp8_sparse_linear_backward(
+            _ptr(dy), ld, _ptr(a_q), DTYPE[_fp8_name(a_dtype)], _ptr(s_a), m, _ptr(packed),
+            DTYPE[_fp8_name(w_dtype)], _ptr(s_w), n, k, _ptr(dx), _ptr(dw), _ptr(dbias),
+            _ptr(workspace), _ws_bytes(workspace, dev), _stream(dev))
+    _check(st, "sfp8_sparse_linear_backward")
+    return dx, dw, dbias
+
+
+def sfp8_gated_linear_backward(dh, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k, act="silu",
+                               bias=None, need_dx=True, need_dw=True, need_dbias=False, dx=None,
+                               dw=None, dbias=None, workspace=None):
+    """Gradients of the gated block from dh [m, n] bf16 and the forward's
+    8-bit checkpoint a_q [m, k], s_a [m]: returns (dx [m, k], dw [2n, k],
+    dbias [2n]), bf16, None where not asked for; dw's and dbias's first n rows
+    are gate's, the others up's."""
+    lib = load_library()
+    _require_cuda(dh, a_q, s_a, packed, s_w, bias)
+    if a_q.dim() != 2:
+        raise ValueError("a_q must be 2-D")
+    m, dev = a_q.shape[0], a_q.device
+    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
+    _tensor(s_a, "s_a", (m,), torch.float32, dev)
+    _gated_args(n, k, packed, s_w, bias, dev)
+    ld = _grad_input(dh, "dh", m, n, dev)
+    dx, dw, dbias = _grad_outputs(m, 2 * n, k, (need_dx, need_dw, need_dbias), (dx, dw, dbias),
+                                  dev)
+    if workspace is None:
+        workspace = new_gated_backward_workspace(m, n, k, dev)
+    with torch.cuda.device(dev):
+        st = lib.sfp8_gated_linear_backward(
+            _ptr(dh), ld, _ptr(a_q), DTYPE[_fp8_name(a_dtype)], _ptr(s_a), m, _ptr(packed),
+            DTYPE[_fp8_name(w_dtype)], _ptr(s_w), n, k, _activation(act), _ptr(bias), _ptr(dx),
+            _ptr(dw), _ptr(dbias), _ptr(workspace), _ws_bytes(workspace, dev), _stream(dev))
+    _check(st, "sfp8_gated_linear_backward")
+    return dx, dw, dbias
 
 
 def sfp8_selftest_timeout(device=None):

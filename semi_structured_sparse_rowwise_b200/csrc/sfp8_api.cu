@@ -20,6 +20,7 @@
 #include "prepare_weight24.cuh"
 #include "sparse_linear.cuh"
 #include "sparse_linear_pair.cuh"
+#include "grad_gemm.cuh"
 
 namespace sfp8 {
 namespace {
@@ -34,6 +35,7 @@ struct DeviceInfo {
   bool smem_attr_set[80] = {};   // (BN, KS, RA, FQ) instantiations, then the gated ones
   int pair_clusters[12] = {};    // co-resident pairs of the pair kernel by (KS, WT) and epilogue
                                  // (0: unknown)
+  int grad_clusters[4] = {};     // the same of the gradient GEMM by (tile width, A's major-ness)
   int tw_blocks[12] = {};        // co-resident CTAs per SM of the tensor-wise quantiser (0: unknown)
   long long l2_bytes = 0;
 };
@@ -578,7 +580,8 @@ LinearPlan make_plan(int dev, int64_t m, int64_t n, int64_t k, int num_sms) {
 struct GatedCall {
   int epi;          // kEpiGated or kEpiGatedGrad
   int act;          // SFP8_ACT_*
-  const void* dh;   // kEpiGatedGrad: [m, hidden] bf16
+  const void* dh;   // kEpiGatedGrad: [m, hidden] bf16, row stride ld_dh
+  int64_t ld_dh;
   int64_t ld_out;   // row stride of the output
 };
 
@@ -832,6 +835,7 @@ sfp8_status launch_pair_cfg(DeviceInfo* dev, const LinearPlan& pl, const void* a
   if (EPI != kEpiLinear) {
     prm.act = gc->act;
     prm.dh = static_cast<const __nv_bfloat16*>(gc->dh);
+    prm.ld_dh = gc->ld_dh;
     prm.ld_out = gc->ld_out;
   }
   return launch_dependent(kern, dim3(2 * pairs), dim3(Cfg::kThreads), pl.smem_bytes, st, tw2,
@@ -1725,7 +1729,7 @@ sfp8_status sfp8_gated_linear(const void* a_q, sfp8_dtype a_dtype, const float* 
   unsigned int* counters = need > 0 ? reinterpret_cast<unsigned int*>(
                                           static_cast<uint8_t*>(workspace) + pl.partial_bytes)
                                     : nullptr;
-  const GatedCall gc{kEpiGated, act, nullptr, n};
+  const GatedCall gc{kEpiGated, act, nullptr, 0, n};
   return launch_linear(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, 2 * n, k, bias, h,
                        static_cast<float*>(workspace), counters,
                        static_cast<cudaStream_t>(stream), nullptr, 0, nullptr, &gc);
@@ -1743,7 +1747,7 @@ sfp8_status sfp8_gated_linear_quant(const void* x, sfp8_dtype x_dtype, int64_t l
                                     void* stream) {
   const sfp8_status s = validate_gated(n, act);
   if (s != SFP8_OK) return s;
-  const GatedCall gc{kEpiGated, act, nullptr, n};
+  const GatedCall gc{kEpiGated, act, nullptr, 0, n};
   return quant_linear(x, x_dtype, ld_x, a_dtype, a_q, s_a, m, packed, w_dtype, s_w, 2 * n, k,
                       bias, h, workspace, workspace_bytes, stream, kQuantChained, &gc);
 }
@@ -1890,3 +1894,5 @@ extern "C" sfp8_status sfp8_sparse_linear_noalloc(const void* a_q, sfp8_dtype a_
                        static_cast<float*>(scratch), reinterpret_cast<unsigned int*>(counters),
                        st);
 }
+
+#include "backward_api.cuh"

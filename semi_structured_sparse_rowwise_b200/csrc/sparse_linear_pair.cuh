@@ -109,7 +109,8 @@ struct PairParams {
   uint32_t idesc;
   // gated forms only: n counts the 2 x hidden rows
   int act;                  // SFP8_ACT_*
-  const __nv_bfloat16* dh;  // [m][n / 2] (kEpiGatedGrad)
+  const __nv_bfloat16* dh;  // [m][ld_dh], n / 2 columns (kEpiGatedGrad)
+  long long ld_dh;
   long long ld_out;         // row stride of y: h's n / 2, dz's padded width
 };
 
@@ -400,7 +401,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
             for (int j = 0; j < 8; ++j)
               dh[j] = (n < p.n && first + j < p.m)
                           ? __bfloat162float(
-                                p.dh[static_cast<long long>(first + j) * (p.n >> 1) + (n >> 1)])
+                                p.dh[static_cast<long long>(first + j) * p.ld_dh + (n >> 1)])
                           : 0.0f;
           }
           tmem_ld_wait();

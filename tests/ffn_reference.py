@@ -75,3 +75,36 @@ def gated_reference(a, s_a, w_rows, s_w, bias, name):
     dg, du = dz[:, 0::2], dz[:, 1::2]
     bound = 1.13 * dg * (up.abs() + du) + (f.abs() + 1.13 * dg) * du
     return gate, up, h, bound + (BF16_HALF_STEP + 2.0 ** -18) * (h.abs() + bound) + 1e-37
+
+
+def backward_reference(dz, dz_err, a, s_a, w, s_w):
+    """dx, dw, db in 64 bits from dz (its own error bound dz_err), each with
+    the bound of its difference: the expanded operands are rounded to bf16
+    once, the fp32 sums err by well under 2^-12 of the products' size, the
+    result is rounded once."""
+    ws = w * s_w.double()[:, None]
+    xs = a * s_a.double()[:, None]
+    out = []
+    for p, e, q in ((dz, dz_err, ws), (dz.t(), dz_err.t(), xs)):
+        ref = p @ q
+        size = (BF16_HALF_STEP + 2.0 ** -12) * (p.abs() @ q.abs()) + 1.01 * (e @ q.abs())
+        out.append((ref, size + BF16_HALF_STEP * (ref.abs() + size) + 1e-37))
+    ref = dz.sum(0)
+    size = 2.0 ** -12 * dz.abs().sum(0) + dz_err.sum(0)
+    out.append((ref, size + BF16_HALF_STEP * (ref.abs() + size) + 1e-37))
+    return out
+
+
+def gated_grad_reference(dh, gate, up, z_err, name):
+    """dz (alternating columns) in 64 bits and its error bound: gate and up err
+    by z_err, act and act' have slopes of at most 1.13 and 0.8 (SiLU's second
+    derivative is at most 1/2, GELU's below 0.8), dz is rounded once."""
+    f, df = act(gate, name)
+    dg, du = z_err[:, 0::2], z_err[:, 1::2]
+    d = dh.double()
+    dgate, dup = d * up * df, d * f
+    e_gate = d.abs() * (du * (df.abs() + 0.8 * dg) + up.abs() * 0.8 * dg + 2.0 ** -18 * up.abs())
+    e_up = d.abs() * (1.13 * dg + 2.0 ** -18 * f.abs())
+    dz = torch.stack((dgate, dup), 2).reshape(dh.shape[0], -1)
+    err = torch.stack((e_gate, e_up), 2).reshape(dh.shape[0], -1)
+    return dz, err + BF16_HALF_STEP * (dz.abs() + err) + 1e-37
