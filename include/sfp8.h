@@ -523,9 +523,11 @@ sfp8_status sfp8_gated_linear_quant(const void* x, sfp8_dtype x_dtype, int64_t l
  * sfp8_gated_linear_backward, from dh [m, n], first
  *     dgate = dh * up * act'(gate),   dup = dh * act(gate)
  * and then the three sums over the 2n rows.
- * Sums are held in fp32 and the results rounded once to bf16.  The operands
- * s_w W_q, s_a A_q and dgate, dup enter the tensor cores as bf16, one
- * rounding (2^-9) each.
+ * Sums are held in fp32 and the results rounded once to bf16.  Scales are
+ * positive, as the quantisers write them.  One operand
+ * of each product is rounded to bf16 on its way to the tensor cores (half a
+ * step of it): s_w W_q and s_a A_q in the plain linear, dgate and dup (with
+ * both scales multiplied in) in the gated block; the other is exact.
  *
  *  dy, dh  device, bf16, row stride ld >= n.  dh: any 2-byte aligned.  dy:
  *          16-byte aligned with ld_dy % 8 == 0, or any if n % 8 != 0 (it is
@@ -559,6 +561,59 @@ sfp8_status sfp8_gated_linear_backward(const void* dh, int64_t ld_dh, const void
                                        sfp8_activation act, const void* bias, void* dx,
                                        void* dw, void* dbias, void* workspace,
                                        size_t workspace_bytes, void* stream);
+
+/*
+ * Layer norm over the rows of x, in front of the quantised linears: to
+ * row-wise FP8 codes (what sfp8_sparse_linear and sfp8_gated_linear take), to
+ * x's type, or both in one call.
+ *     mean = sum_c x / cols,   rstd = 1 / sqrt(sum_c (x - mean)^2 / cols + eps)
+ *     y    = (x - mean) * rstd * weight + bias                  (fp32)
+ *     codes and scales: those of sfp8_quantize_rowwise for the fp32 y (not for
+ *     y after its rounding to x's type)
+ *
+ *  x       device, [rows, cols] of x_dtype (BF16, F16 or F32), row stride
+ *          ld_x >= cols.  cols >= 1, any; with q, cols % 16 == 0 and x as for
+ *          sfp8_quantize_rowwise (16-byte aligned base and rows).  Rows that
+ *          are 16-byte aligned (cols, ld_x and every buffer) are read 16
+ *          bytes at a time.
+ *  weight, bias  device, [cols] of p_dtype, which is x_dtype or F32, or NULL
+ *          (ones, zeros); aligned to their element.
+ *  eps     >= 0 and finite.  A constant row with eps 0 gives NaN (0 * inf).
+ *  y       device, [rows, cols] of x_dtype, or NULL.
+ *  q, q_dtype, scales  device, [rows, cols] codes and [rows] float32, or q
+ *          NULL (scales and q_dtype are then not looked at).
+ *  mean, rstd  device, [rows] float32 each, or NULL; the backward pass takes
+ *          them.
+ * Outputs must not overlap x, the parameters or each other.
+ */
+sfp8_status sfp8_layernorm(const void* x, sfp8_dtype x_dtype, int64_t rows, int64_t cols,
+                           int64_t ld_x, const void* weight, const void* bias,
+                           sfp8_dtype p_dtype, float eps, void* y, void* q,
+                           sfp8_dtype q_dtype, float* scales, float* mean, float* rstd,
+                           void* stream);
+
+/*
+ * Its backward pass, with xh = (x - mean) * rstd and g = weight * dy:
+ *     dx      = rstd * (g - sum_c g / cols - xh * sum_c (g xh) / cols)
+ *     dweight = sum_rows dy * xh,   dbias = sum_rows dy
+ * (the gradient of y; codes are passed straight through).  Sums in fp32, in
+ * an order that depends on the sizes and the device only.
+ *
+ *  dy      device, [rows, cols] of x_dtype, row stride ld_dy >= cols.
+ *  x, ld_x, weight, p_dtype: as in the forward call; mean, rstd from it.
+ *  dx      device, [rows, cols] of x_dtype, or NULL: not computed.
+ *  dweight, dbias  device, [cols] float32, or NULL.
+ *  workspace  16-byte aligned, >= sfp8_layernorm_backward_workspace_bytes(rows,
+ *          cols); needs no clearing.  Calls that share one must not overlap.
+ *  rows == 0: dweight and dbias are zeros.
+ */
+size_t sfp8_layernorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+sfp8_status sfp8_layernorm_backward(const void* dy, int64_t ld_dy, const void* x,
+                                    sfp8_dtype x_dtype, int64_t rows, int64_t cols,
+                                    int64_t ld_x, const void* weight, sfp8_dtype p_dtype,
+                                    const float* mean, const float* rstd, void* dx,
+                                    float* dweight, float* dbias, void* workspace,
+                                    size_t workspace_bytes, void* stream);
 
 /*
  * The layer's forward from host memory to host memory in one call: on

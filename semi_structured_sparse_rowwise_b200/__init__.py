@@ -26,7 +26,9 @@ from .binding import (Sfp8Error, load_library, library_path, new_workspace,
                       new_gated_workspace, new_gated_quant_workspace, sfp8_gated_linear,
                       sfp8_gated_linear_quant, new_linear_backward_workspace,
                       new_gated_backward_workspace, sfp8_sparse_linear_backward,
-                      sfp8_gated_linear_backward, sfp8_read_device_status, sfp8_selftest_timeout,
+                      sfp8_gated_linear_backward, sfp8_layernorm, sfp8_layernorm_quant,
+                      new_layernorm_backward_workspace, sfp8_layernorm_backward,
+                      sfp8_read_device_status, sfp8_selftest_timeout,
                       sfp8_status_string, sfp8_layout_version)
 from .layer import HostPipeline, SparseFp8Linear
 
@@ -49,6 +51,8 @@ __all__ = [
     "sfp8_prepare_gated_weight_24", "new_gated_workspace", "new_gated_quant_workspace",
     "sfp8_gated_linear", "sfp8_gated_linear_quant", "new_linear_backward_workspace",
     "new_gated_backward_workspace", "sfp8_sparse_linear_backward", "sfp8_gated_linear_backward",
+    "sfp8_layernorm", "sfp8_layernorm_quant", "new_layernorm_backward_workspace",
+    "sfp8_layernorm_backward",
     "sfp8_read_device_status", "sfp8_selftest_timeout", "sfp8_status_string",
     "sfp8_layout_version", "SparseFp8Linear", "HostPipeline",
 ]

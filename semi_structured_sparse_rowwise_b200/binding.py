@@ -105,6 +105,13 @@ SIGNATURES = {
                                           _c_void_p, _i32, _c_void_p, _i64, _i64, _i32,
                                           _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
                                           _sz, _c_void_p]),
+    "sfp8_layernorm": (_i32, [_c_void_p, _i32, _i64, _i64, _i64, _c_void_p, _c_void_p, _i32,
+                              ctypes.c_float, _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p,
+                              _c_void_p, _c_void_p]),
+    "sfp8_layernorm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "sfp8_layernorm_backward": (_i32, [_c_void_p, _i64, _c_void_p, _i32, _i64, _i64, _i64,
+                                       _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p,
+                                       _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p]),
     "sfp8_selftest_timeout": (_i32, [_c_void_p]),
     "sfp8_sparse_linear_quant_host": (_i32, [_c_void_p, _c_void_p, _i32, _i32, _c_void_p,
                                              _c_void_p, _i64, _c_void_p, _i32, _c_void_p, _i64,
@@ -838,6 +845,127 @@ def sfp8_gated_linear_backward(dh, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k
             _ptr(dw), _ptr(dbias), _ptr(workspace), _ws_bytes(workspace, dev), _stream(dev))
     _check(st, "sfp8_gated_linear_backward")
     return dx, dw, dbias
+
+
+# ---------------------------------------------------------------- layer norm
+
+
+def _norm_input(x, what):
+    _require_cuda(x)
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError("%s must be 2-D with unit column stride" % what)
+    xd = TORCH_WIDE.get(x.dtype)
+    if xd is None:
+        raise ValueError("%s dtype must be bfloat16, float16 or float32" % what)
+    return xd, x.stride(0) if x.shape[0] > 1 else x.shape[1]
+
+
+def _norm_params(weight, bias, x):
+    """The parameters' common dtype name (x's or f32)."""
+    dtype = None
+    for t, what in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        dtype = t.dtype if dtype is None else dtype
+        if t.dtype != dtype or t.dtype not in (x.dtype, torch.float32):
+            raise ValueError("weight and bias must both have x's dtype, or both float32")
+        _tensor(t, what, (x.shape[1],), t.dtype, x.device)
+    return TORCH_WIDE[x.dtype if dtype is None else dtype]
+
+
+def _norm_call(x, weight, bias, eps, y, q, q_dtype, scales, mean, rstd):
+    lib = load_library()
+    xd, ld = _norm_input(x, "x")
+    pd = _norm_params(weight, bias, x)
+    rows, cols = x.shape
+    for t, what, dtype, shape in ((y, "out", x.dtype, (rows, cols)),
+                                  (q, "q", torch.uint8, (rows, cols)),
+                                  (scales, "scales", torch.float32, (rows,)),
+                                  (mean, "mean", torch.float32, (rows,)),
+                                  (rstd, "rstd", torch.float32, (rows,))):
+        if t is not None:
+            _tensor(t, what, shape, dtype, x.device)
+    with torch.cuda.device(x.device):
+        st = lib.sfp8_layernorm(_ptr(x), DTYPE[xd], rows, cols, ld, _ptr(weight), _ptr(bias),
+                                DTYPE[pd], eps, _ptr(y), _ptr(q), DTYPE[_fp8_name(q_dtype)],
+                                _ptr(scales), _ptr(mean), _ptr(rstd), _stream(x.device))
+    _check(st, "sfp8_layernorm")
+
+
+def sfp8_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, mean=None, rstd=None):
+    """Layer norm of x [rows, cols] bf16/f16/f32 (unit column stride), weight
+    and bias [cols] of x's dtype or float32: returns (y of x's dtype, mean
+    [rows], rstd [rows] float32)."""
+    _norm_input(x, "x")
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    if mean is None:
+        mean = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
+    _norm_call(x, weight, bias, eps, out, None, "e4m3", None, mean, rstd)
+    return out, mean, rstd
+
+
+def sfp8_layernorm_quant(x, weight=None, bias=None, eps=1e-5, q_dtype="e4m3", q=None, scales=None,
+                         mean=None, rstd=None, out=None):
+    """Layer norm of x straight to row-wise FP8 codes, the input of the linear
+    and the gated block: returns (q [rows, cols] uint8, scales, mean, rstd
+    [rows] float32).  A given `out` also receives y in x's dtype."""
+    _norm_input(x, "x")
+    rows = x.shape[0]
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
+    if scales is None:
+        scales = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    if mean is None:
+        mean = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    if rstd is None:
+        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
+    _norm_call(x, weight, bias, eps, out, q, q_dtype, scales, mean, rstd)
+    return q, scales, mean, rstd
+
+
+def new_layernorm_backward_workspace(rows, cols, device):
+    """A workspace for sfp8_layernorm_backward on `device`."""
+    with torch.cuda.device(device):
+        nbytes = int(load_library().sfp8_layernorm_backward_workspace_bytes(rows, cols))
+    return torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=device)
+
+
+def sfp8_layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None,
+                            workspace=None):
+    """Gradients of layer norm from dy [rows, cols] (x's dtype) and the
+    forward's x, weight (or None), mean and rstd: returns (dx of x's dtype,
+    dweight, dbias [cols] float32)."""
+    lib = load_library()
+    xd, ld_x = _norm_input(x, "x")
+    dyd, ld_dy = _norm_input(dy, "dy")
+    if dyd != xd or dy.shape != x.shape or dy.device != x.device:
+        raise ValueError("dy must have x's shape, dtype and device")
+    pd = _norm_params(weight, None, x)
+    rows, cols = x.shape
+    dev = x.device
+    _tensor(mean, "mean", (rows,), torch.float32, dev)
+    _tensor(rstd, "rstd", (rows,), torch.float32, dev)
+    if dx is None:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    if dweight is None:
+        dweight = torch.empty((cols,), dtype=torch.float32, device=dev)
+    if dbias is None:
+        dbias = torch.empty((cols,), dtype=torch.float32, device=dev)
+    _tensor(dx, "dx", (rows, cols), x.dtype, dev)
+    _tensor(dweight, "dweight", (cols,), torch.float32, dev)
+    _tensor(dbias, "dbias", (cols,), torch.float32, dev)
+    if workspace is None:
+        workspace = new_layernorm_backward_workspace(rows, cols, dev)
+    with torch.cuda.device(dev):
+        st = lib.sfp8_layernorm_backward(
+            _ptr(dy), ld_dy, _ptr(x), DTYPE[xd], rows, cols, ld_x, _ptr(weight), DTYPE[pd],
+            _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
+            _ws_bytes(workspace, dev), _stream(dev))
+    _check(st, "sfp8_layernorm_backward")
+    return dx, dweight, dbias
 
 
 def sfp8_selftest_timeout(device=None):

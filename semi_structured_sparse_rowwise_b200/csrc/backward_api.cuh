@@ -121,11 +121,11 @@ unsigned grid_for(int64_t items, int per_block, const DeviceInfo* dev, int block
 
 // D [rows, cols] = sum over t < contraction of A[r, t] B[t, c].  A is
 // [rows][lda] (a_mn false) or [contraction][lda] (a_mn true), B is
-// [contraction][cols].
+// [contraction][cols]; row_scale [rows] is divided out of D (or null).
 sfp8_status launch_grad_gemm(DeviceInfo* dev, const GradPlan& pl, const void* a, int64_t lda,
                              bool a_mn, const void* b, int64_t rows, int64_t cols,
-                             int64_t contraction, void* d, int64_t pair_rows, float* partial,
-                             cudaStream_t st) {
+                             int64_t contraction, const float* row_scale, void* d,
+                             int64_t pair_rows, float* partial, cudaStream_t st) {
   CUtensorMap ta, tb;
   sfp8_status s = a_mn ? encode_bf16_2d(&ta, a, rows, contraction, lda, kGgStageK)
                        : encode_bf16_2d(&ta, a, contraction, rows, lda, 128);
@@ -145,6 +145,7 @@ sfp8_status launch_grad_gemm(DeviceInfo* dev, const GradPlan& pl, const void* a,
   prm.items = pl.m_tiles * pl.n_tiles * pl.splits;
   // about as many row tiles as column tiles in flight at a time
   prm.band = 8;
+  prm.row_scale = row_scale;
   prm.pair_rows = static_cast<int>(pair_rows);
   if (pl.bn == 256)
     s = a_mn ? launch_grad_gemm_cfg<256, true>(dev, ta, tb, prm, st)
@@ -155,7 +156,7 @@ sfp8_status launch_grad_gemm(DeviceInfo* dev, const GradPlan& pl, const void* a,
   if (s != SFP8_OK || pl.splits == 1) return s;
   return launch_dependent(grad_gemm_join_kernel, dim3(grid_for(rows * (cols / 8), 256, dev, 8)),
                           dim3(256), 0, st, static_cast<const float*>(partial), pl.splits,
-                          static_cast<int>(rows), static_cast<int>(cols),
+                          static_cast<int>(rows), static_cast<int>(cols), row_scale,
                           static_cast<__nv_bfloat16*>(d), static_cast<long long>(cols),
                           static_cast<int>(pair_rows));
 }
@@ -221,34 +222,37 @@ struct BackwardCall {
 
 // dx, dw and dbias from dz [m, rows] (row stride ld, 16-byte aligned, ld a
 // multiple of 8): expand the weight, dx; expand the checkpoint, dw; column
-// sums.  pair_rows: n for a gated block (dw and dbias leave in gate-then-up
-// order), else 0.
+// sums.  pair_rows: n for a gated block (dz then holds both scales, dw and
+// dbias leave in gate-then-up order), else 0.
 sfp8_status launch_linear_grads(DeviceInfo* dev, const BackwardPlan& bp, const BackwardCall& c,
                                 const void* dz, int64_t ld, int64_t pair_rows, uint8_t* ws,
                                 cudaStream_t st) {
   __nv_bfloat16* expanded = reinterpret_cast<__nv_bfloat16*>(ws + bp.expand_off);
   float* partial = reinterpret_cast<float*>(ws + bp.partial_off);
   sfp8_status s = SFP8_OK;
+  // the scales are in the expanded operand, or in dz and divided out
+  const bool scaled_dz = pair_rows != 0;
+  const float* none = nullptr;
   if (c.dx != nullptr) {
     auto kern = c.w_dtype == SFP8_E5M2 ? expand_weight_kernel<SFP8_E5M2>
                                        : expand_weight_kernel<SFP8_E4M3>;
     s = launch_dependent(kern, dim3(grid_for(c.rows * (c.k / 32), 256, dev, 8)), dim3(256), 0, st,
-                         static_cast<const uint8_t*>(c.packed), c.s_w,
+                         static_cast<const uint8_t*>(c.packed), scaled_dz ? none : c.s_w,
                          static_cast<long long>(c.rows), static_cast<long long>(c.k), expanded);
     if (s != SFP8_OK) return s;
-    s = launch_grad_gemm(dev, bp.dx, dz, ld, false, expanded, c.m, c.k, c.rows, c.dx, 0, partial,
-                         st);
+    s = launch_grad_gemm(dev, bp.dx, dz, ld, false, expanded, c.m, c.k, c.rows,
+                         scaled_dz ? c.s_a : none, c.dx, 0, partial, st);
     if (s != SFP8_OK) return s;
   }
   if (c.dw != nullptr) {
     auto kern = c.a_dtype == SFP8_E5M2 ? expand_rows_kernel<SFP8_E5M2>
                                        : expand_rows_kernel<SFP8_E4M3>;
     s = launch_dependent(kern, dim3(grid_for(c.m * (c.k / 16), 256, dev, 8)), dim3(256), 0, st,
-                         static_cast<const uint8_t*>(c.a_q), c.s_a, static_cast<long long>(c.m),
-                         static_cast<long long>(c.k), expanded);
+                         static_cast<const uint8_t*>(c.a_q), scaled_dz ? none : c.s_a,
+                         static_cast<long long>(c.m), static_cast<long long>(c.k), expanded);
     if (s != SFP8_OK) return s;
-    s = launch_grad_gemm(dev, bp.dw, dz, ld, true, expanded, c.rows, c.k, c.m, c.dw, pair_rows,
-                         partial, st);
+    s = launch_grad_gemm(dev, bp.dw, dz, ld, true, expanded, c.rows, c.k, c.m,
+                         scaled_dz ? c.s_w : none, c.dw, pair_rows, partial, st);
     if (s != SFP8_OK) return s;
   }
   if (c.dbias != nullptr) {
@@ -258,12 +262,12 @@ sfp8_status launch_linear_grads(DeviceInfo* dev, const BackwardPlan& bp, const B
                               static_cast<unsigned>(bp.runs)),
                          dim3(256), 0, st, static_cast<const __nv_bfloat16*>(dz),
                          static_cast<long long>(c.m), static_cast<long long>(c.rows),
-                         static_cast<long long>(ld), sums);
+                         static_cast<long long>(ld), scaled_dz ? c.s_a : none, sums);
     if (s != SFP8_OK) return s;
     s = launch_dependent(column_sums_join_kernel,
                          dim3(static_cast<unsigned>((c.rows + 255) / 256)), dim3(256), 0, st,
                          static_cast<const float*>(sums), bp.runs, static_cast<long long>(c.rows),
-                         static_cast<__nv_bfloat16*>(c.dbias),
+                         scaled_dz ? c.s_w : none, static_cast<__nv_bfloat16*>(c.dbias),
                          static_cast<long long>(pair_rows));
   }
   return s;

@@ -10,7 +10,17 @@
 // accumulator lanes of one warp, whatever the work split: whole tiles, CTA
 // pairs and split-K finishers all end in the same 16-token chunk, and one
 // shuffle with the neighbour lane pairs them.  z never leaves the registers
-// and is not rounded; h (and dz) is rounded once, to bf16, as it is stored.
+// and is not rounded; h is rounded once, to bf16, as it is stored.
+//
+// dz is stored as bf16 of dz[m, r] * s_a[m] * s_w[r].  With both scales in
+// it, the FP8 codes themselves are the other operand of both gradient
+// products -- exact in bf16, where the scaled weight or activation would be
+// rounded once more -- and what each product has too much is constant along
+// its output rows (s_a[m] in dx, s_w[r] in dw), so it is divided out of the
+// fp32 sums:
+//     dx[m, k] = 1 / s_a[m] * sum_r dz'[m, r] W_q[r, k]
+//     dw[r, k] = 1 / s_w[r] * sum_m dz'[m, r] A_q[m, k]
+// Scales are at least 1e-12 / 57344, so dz' and the quotients stay in range.
 //
 // Of a chunk's 16 tokens the gate lane finishes tokens 0..7 and the up lane
 // 8..15: each sends its neighbour the eight values that one needs (8 shuffles

@@ -1,7 +1,7 @@
 // The dense products of the backward pass, bf16 in, fp32 accumulation, bf16
 // out, on CTA pairs (tcgen05 kind::f16, cta_group::2).
 //
-//     D[r, c] = sum_t A[r, t] * B[t, c]
+//     D[r, c] = 1 / scale[r] * sum_t A[r, t] * B[t, c]      (scale optional)
 //
 //   input gradient    dx[m, k] = sum_r dz[m, r] * What[r, k]
 //                     A = dz, contraction index contiguous (K-major);
@@ -75,6 +75,7 @@ struct GgParams {
   int items;              // m_tiles * n_tiles * splits
   int pairs;              // gridDim.x / 2
   int band;               // row tiles per band of the tile order
+  const float* row_scale; // [rows], divided out of D's rows; or null
   int pair_rows;          // != 0: D's row r is stored at row (r & 1) * pair_rows + r / 2
   uint32_t idesc;
 };
@@ -297,6 +298,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
       int mt, nt, sp;
       gg_item(p, it, mt, nt, sp);
       const int r = mt * kGgTileM + static_cast<int>(rank) * 128 + q * 32 + lane;
+      const float rs = p.row_scale != nullptr && r < p.rows ? 1.0f / __ldg(p.row_scale + r) : 1.0f;
       int ok = 1;
       if (lane == 0) ok = mbar_wait(smem_u32(&accf_bar[acc]), acc_phase, abort_flag) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -329,8 +331,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
             uint32_t w[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(__uint_as_float(v[h][2 * j]),
-                                                              __uint_as_float(v[h][2 * j + 1]));
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(
+                  __uint_as_float(v[h][2 * j]) * rs, __uint_as_float(v[h][2 * j + 1]) * rs);
               w[j] = *reinterpret_cast<const uint32_t*>(&b2);
             }
             __nv_bfloat16* dst = p.d + out_row * p.ld_d + col;
@@ -354,11 +356,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
   if (warp == kGgMmaWarp) tmem_dealloc_pair(tmem_base, 2 * BN);
 }
 
-// D = the sum of the splits' partial sums, in split order, rounded once.
+// D = the sum of the splits' partial sums, in split order, scaled and rounded
+// once.
 // One thread per 8 columns.
 __global__ void __launch_bounds__(256)
     grad_gemm_join_kernel(const float* __restrict__ partial, int splits, int rows, int cols,
-                          __nv_bfloat16* __restrict__ d, long long ld_d, int pair_rows) {
+                          const float* __restrict__ row_scale, __nv_bfloat16* __restrict__ d,
+                          long long ld_d, int pair_rows) {
   grid_dependents_launch();
   grid_dependency_wait();
   const long long vecs = static_cast<long long>(rows) * (cols / 8);
@@ -375,10 +379,11 @@ __global__ void __launch_bounds__(256)
       s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
       s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
     }
+    const float rs = row_scale != nullptr ? 1.0f / row_scale[r] : 1.0f;
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(s[2 * j], s[2 * j + 1]);
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(s[2 * j] * rs, s[2 * j + 1] * rs);
       w[j] = *reinterpret_cast<const uint32_t*>(&b2);
     }
     long long row = r;
@@ -399,10 +404,10 @@ __device__ __forceinline__ float2 fp8_pair_to_float(uint32_t codes) {
 
 // The expanded weight What[r, k] = bf16(dec(W_q[r, k]) * s_w[r]), dense: one
 // thread per 32 k of a row (16 kept codes, 8 index nibbles), reading the
-// packed tile and writing 64 contiguous bytes.  The one rounding (2^-9
-// relative at most) is that of the bf16 operand; the product in fp32 is
-// rounded once more, 2^-24.  What has the weight's true rows only (padding
-// rows are not written).
+// packed tile and writing 64 contiguous bytes.  With s_w the one rounding
+// (half a bf16 step) is that of the operand; without it (null: the scales are
+// in dz) the codes are exact in bf16.  What has the weight's true rows only
+// (padding rows are not written).
 template <int kFmt>
 __global__ void __launch_bounds__(256)
     expand_weight_kernel(const uint8_t* __restrict__ packed, const float* __restrict__ s_w,
@@ -422,7 +427,7 @@ __global__ void __launch_bounds__(256)
     const uint4 v = __ldg(
         reinterpret_cast<const uint4*>(tile + 64 * r + (16 * j ^ (16 * (r >> 1 & 3)))));
     const uint32_t meta = __ldg(reinterpret_cast<const uint32_t*>(tile + 8192 + 16 * r + 4 * j));
-    const float s = __ldg(s_w + row);
+    const float s = s_w != nullptr ? __ldg(s_w + row) : 1.0f;
     const uint32_t vals[4] = {v.x, v.y, v.z, v.w};
     uint32_t w[16];
 #pragma unroll
@@ -445,8 +450,8 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// The expanded checkpoint xhat[m, k] = bf16(dec(A_q[m, k]) * s_a[m]): one
-// thread per 16 codes.
+// The expanded checkpoint xhat[m, k] = bf16(dec(A_q[m, k]) * s_a[m]), or with
+// s null the codes' own values: one thread per 16 codes.
 template <int kFmt>
 __global__ void __launch_bounds__(256)
     expand_rows_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s, long long rows,
@@ -458,7 +463,7 @@ __global__ void __launch_bounds__(256)
   for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
        i += static_cast<long long>(gridDim.x) * blockDim.x) {
     const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + i);
-    const float sc = __ldg(s + i / per_row);
+    const float sc = s != nullptr ? __ldg(s + i / per_row) : 1.0f;
     const uint32_t in[4] = {v.x, v.y, v.z, v.w};
     uint32_t w[8];
 #pragma unroll
@@ -492,11 +497,13 @@ __global__ void __launch_bounds__(256)
 // Column sums of dz [rows][ld] for the bias gradient, in fp32, in two steps:
 // block (x, y) adds the rows of its run y for 64 columns (8 row lanes x 32
 // column pairs) into partial[y][cols]; the second kernel adds the runs in
-// order and rounds once.
+// order and rounds once.  row_scale and col_scale, where given, are divided
+// out (a gated block's dz holds both).
 constexpr int kColSumCols = 64;
 __global__ void __launch_bounds__(256)
     column_sums_kernel(const __nv_bfloat16* __restrict__ dz, long long rows, long long cols,
-                       long long ld, float* __restrict__ partial) {
+                       long long ld, const float* __restrict__ row_scale,
+                       float* __restrict__ partial) {
   grid_dependents_launch();
   grid_dependency_wait();
   __shared__ float2 sums[8][32];
@@ -509,13 +516,15 @@ __global__ void __launch_bounds__(256)
     for (long long r = r0 + y; r < r1; r += 8) {
       const float2 v =
           __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(dz + r * ld + col));
-      s.x += v.x;
-      s.y += v.y;
+      const float rs = row_scale != nullptr ? 1.0f / row_scale[r] : 1.0f;
+      s.x = fmaf(v.x, rs, s.x);
+      s.y = fmaf(v.y, rs, s.y);
     }
   } else if (col < cols) {
     for (long long r = r0 + y; r < r1; r += 8) {
-      s.x += __bfloat162float(dz[r * ld + col]);
-      if (col + 1 < cols) s.y += __bfloat162float(dz[r * ld + col + 1]);
+      const float rs = row_scale != nullptr ? 1.0f / row_scale[r] : 1.0f;
+      s.x = fmaf(__bfloat162float(dz[r * ld + col]), rs, s.x);
+      if (col + 1 < cols) s.y = fmaf(__bfloat162float(dz[r * ld + col + 1]), rs, s.y);
     }
   }
   sums[y][x] = s;
@@ -535,13 +544,14 @@ __global__ void __launch_bounds__(256)
 // (c & 1) * pair_rows + c / 2 (a gated block's gate and up values).
 __global__ void __launch_bounds__(256)
     column_sums_join_kernel(const float* __restrict__ partial, int runs, long long cols,
-                            __nv_bfloat16* __restrict__ out, long long pair_rows) {
+                            const float* __restrict__ col_scale, __nv_bfloat16* __restrict__ out, long long pair_rows) {
   grid_dependents_launch();
   grid_dependency_wait();
   const long long c = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
   if (c >= cols) return;
   float s = 0.0f;
   for (int y = 0; y < runs; ++y) s += partial[y * cols + c];
+  if (col_scale != nullptr) s /= col_scale[c];
   long long at = c;
   if (pair_rows != 0) at = (c & 1) ? pair_rows + (c >> 1) : (c >> 1);
   out[at] = __float2bfloat16_rn(s);

@@ -21,6 +21,7 @@
 #include "sparse_linear.cuh"
 #include "sparse_linear_pair.cuh"
 #include "grad_gemm.cuh"
+#include "layernorm.cuh"
 
 namespace sfp8 {
 namespace {
@@ -36,6 +37,8 @@ struct DeviceInfo {
   int pair_clusters[12] = {};    // co-resident pairs of the pair kernel by (KS, WT) and epilogue
                                  // (0: unknown)
   int grad_clusters[4] = {};     // the same of the gradient GEMM by (tile width, A's major-ness)
+  int norm_blocks[32] = {};      // co-resident CTAs per SM of the layer norm backward by (type,
+                                 // row split) (0: unknown)
   int tw_blocks[12] = {};        // co-resident CTAs per SM of the tensor-wise quantiser (0: unknown)
   long long l2_bytes = 0;
 };
@@ -1896,3 +1899,4 @@ extern "C" sfp8_status sfp8_sparse_linear_noalloc(const void* a_q, sfp8_dtype a_
 }
 
 #include "backward_api.cuh"
+#include "layernorm_api.cuh"

@@ -368,6 +368,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
       const float sw = (n < p.n) ? __ldg(p.s_w + n) : 0.0f;
       const long long bias_at = EPI != kEpiLinear ? gated_bias_index(n, p.n) : n;
       const float bv = (p.bias != nullptr && n < p.n) ? __bfloat162float(p.bias[bias_at]) : 0.0f;
+      float sw_gate = 0.0f, sw_up = 0.0f;
+      if constexpr (EPI == kEpiGatedGrad) {
+        const float other = __shfl_xor_sync(0xffffffffu, sw, 1);
+        sw_gate = (n & 1) ? other : sw;
+        sw_up = (n & 1) ? sw : other;
+      }
       int ok = 1;
       if (lane == 0) ok = mbar_wait(smem_u32(&accf_bar[acc]), acc_phase, abort_flag) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -419,9 +425,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
               } else {
                 float f, df;
                 act_value_grad(g[j], p.act, f, df);
-                // gate's and up's gradient, neighbours in dz
+                // gate's and up's gradient with the scales in, neighbours in dz
+                const float d = dh[j] * ((n & 1) ? sa[j + 8] : sa[j]);
                 *reinterpret_cast<__nv_bfloat162*>(row + (n & ~1)) =
-                    __floats2bfloat162_rn(dh[j] * u[j] * df, dh[j] * f);
+                    __floats2bfloat162_rn(d * u[j] * df * sw_gate, d * f * sw_up);
               }
             }
           }
