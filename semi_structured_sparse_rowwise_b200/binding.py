@@ -609,7 +609,34 @@ def _quant_linear(name, x, a_dtype, packed, w_dtype, s_w, n, k, bias, out, works
     return out, a_q, s_a
 
 
-# ---------------------------------------------------------------- gated feed-forward block
+# ---------------------------------------------------------------- feed-forward sublayer
+# The wrappers below are called once a layer and token in serving, where the
+# host's share of a call is as long as its kernels.  They pass plain integers
+# for pointers and read the device and the raw stream directly: together with
+# the checks about 10 us a call, where torch's device context manager, stream
+# object and ctypes pointer objects alone take that long.
+
+
+def _run(name, device, *args):
+    """Calls the library on `device`'s current stream (the last argument) and
+    raises on a status other than OK."""
+    fn = getattr(load_library(), name)
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if status != OK:
+        raise Sfp8Error(status, name)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _fp8(dtype):
+    return DTYPE[_fp8_name(dtype)]
 
 
 def _activation(act):
@@ -619,16 +646,40 @@ def _activation(act):
 
 
 def _tensor(t, what, shape, dtype, device):
-    """Refuses anything but a contiguous tensor of this shape, dtype and device."""
-    if (tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous()
-            or t.device != torch.device(device)):
+    """Refuses anything but a contiguous CUDA tensor of this shape (a tuple),
+    dtype and device."""
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor of shape %s on %s"
                          % (what, dtype, tuple(shape), device))
 
 
+def _out(t, what, shape, dtype, device):
+    """A given output, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _tensor(t, what, shape, dtype, device)
+    return t
+
+
+def _rows_in(x, what, cols=None):
+    """A 2-D CUDA input with unit column stride: its type's code, its row stride."""
+    dtype = TORCH_WIDE.get(x.dtype)
+    if dtype is None:
+        raise ValueError("%s dtype must be bfloat16, float16 or float32" % what)
+    if not x.is_cuda or x.dim() != 2 or (cols is not None and x.shape[1] != cols):
+        raise ValueError("%s must be a 2-D CUDA tensor%s"
+                         % (what, "" if cols is None else " with %d columns" % cols))
+    ld, unit = x.stride()
+    if unit != 1 and x.shape[1] > 1:
+        raise ValueError("%s must have unit column stride" % what)
+    return DTYPE[dtype], ld if x.shape[0] > 1 else x.shape[1]
+
+
 def _weight(packed, s_w, rows, k, device):
     """The compressed weight of `rows` rows and its scales, on `device`."""
-    need = load_library().sfp8_compressed_bytes(rows, k)
+    if rows < 0 or k < 0:
+        raise ValueError("n and k must not be negative")
+    need = (rows + 127) // 128 * 128 * k * 5 // 8
     if (packed.device != device or packed.dtype != torch.uint8 or not packed.is_contiguous()
             or packed.numel() < need):
         raise ValueError("packed must be a contiguous uint8 tensor of at least %d bytes on %s"
@@ -636,58 +687,66 @@ def _weight(packed, s_w, rows, k, device):
     _tensor(s_w, "s_w", (rows,), torch.float32, device)
 
 
-def _gated_args(n, k, packed, s_w, bias, device):
-    if n < 0:
-        raise ValueError("n must not be negative")
-    _weight(packed, s_w, 2 * n, k, device)
-    if bias is not None:
-        _tensor(bias, "bias", (2 * n,), torch.bfloat16, device)
+def _codes(a_q, s_a, k):
+    """A quantised activation [m, k] and its scales: its rows and device."""
+    if not a_q.is_cuda or a_q.dim() != 2:
+        raise ValueError("a_q must be a 2-D CUDA tensor")
+    m, dev = a_q.shape[0], a_q.device
+    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
+    _tensor(s_a, "s_a", (m,), torch.float32, dev)
+    return m, dev
+
+
+def _workspace(ws, device):
+    """Address and size of a caller's workspace."""
+    return ws.data_ptr(), _ws_bytes(ws, device)
+
+
+def _new_workspace(query, sizes, device):
+    with torch.cuda.device(device):
+        nbytes = int(query(*sizes))
+    return torch.zeros((max(nbytes, 16),), dtype=torch.uint8, device=device)
+
+
+# ---- gated block
 
 
 def sfp8_prepare_gated_weight_24(w_gate, w_up, q_dtype="e4m3", packed=None, scales=None):
     """w_gate, w_up [n, k] bf16/f16/f32 (unit column stride, the same type and
     strides) -> (packed, s_w): the compressed weight of a gated block, 2n rows
     that alternate gate and up, each prepared as by sfp8_prepare_weight_24."""
-    lib = load_library()
-    _require_cuda(w_gate, w_up)
-    if w_gate.dim() != 2 or w_gate.stride(1) != 1:
-        raise ValueError("w_gate must be 2-D with unit column stride")
+    wd, ld = _rows_in(w_gate, "w_gate")
     if (w_up.shape != w_gate.shape or w_up.dtype != w_gate.dtype or w_up.device != w_gate.device
-            or w_up.stride(1) != 1 or (w_gate.shape[0] > 1 and w_up.stride(0) != w_gate.stride(0))):
+            or _rows_in(w_up, "w_up")[1] != ld):
         raise ValueError("w_up must have w_gate's shape, dtype, device and strides")
-    wd = TORCH_WIDE.get(w_gate.dtype)
-    if wd is None:
-        raise ValueError("weight dtype must be bfloat16, float16 or float32")
     n, k = w_gate.shape
+    dev = w_gate.device
     if packed is None:
-        packed = torch.empty((lib.sfp8_compressed_bytes(2 * n, k),), dtype=torch.uint8,
-                             device=w_gate.device)
+        packed = torch.empty((load_library().sfp8_compressed_bytes(2 * n, k),),
+                             dtype=torch.uint8, device=dev)
     if scales is None:
-        scales = torch.empty((2 * n,), dtype=torch.float32, device=w_gate.device)
-    _weight(packed, scales, 2 * n, k, w_gate.device)
-    ld = w_gate.stride(0) if n > 1 else k
-    with torch.cuda.device(w_gate.device):
-        st = lib.sfp8_prepare_gated_weight_24(_ptr(w_gate), _ptr(w_up), DTYPE[wd], n, k, ld,
-                                              DTYPE[_fp8_name(q_dtype)], _ptr(packed),
-                                              _ptr(scales), _stream(w_gate.device))
-    _check(st, "sfp8_prepare_gated_weight_24")
+        scales = torch.empty((2 * n,), dtype=torch.float32, device=dev)
+    _weight(packed, scales, 2 * n, k, dev)
+    _run("sfp8_prepare_gated_weight_24", dev, _addr(w_gate), _addr(w_up), wd, n, k, ld,
+         _fp8(q_dtype), _addr(packed), _addr(scales))
     return packed, scales
-
-
-def _new_workspace(query, m, n, k, device):
-    with torch.cuda.device(device):
-        nbytes = int(query(m, n, k))
-    return torch.zeros((max(nbytes, 16),), dtype=torch.uint8, device=device)
 
 
 def new_gated_workspace(m, n, k, device):
     """A zeroed workspace for sfp8_gated_linear(m, n, k) on `device`."""
-    return _new_workspace(load_library().sfp8_gated_linear_workspace_bytes, m, n, k, device)
+    return _new_workspace(load_library().sfp8_gated_linear_workspace_bytes, (m, n, k), device)
 
 
 def new_gated_quant_workspace(m, n, k, device):
     """A zeroed workspace for sfp8_gated_linear_quant(m, n, k) on `device`."""
-    return _new_workspace(load_library().sfp8_gated_linear_quant_workspace_bytes, m, n, k, device)
+    return _new_workspace(load_library().sfp8_gated_linear_quant_workspace_bytes, (m, n, k),
+                          device)
+
+
+def _gated_weight(n, k, packed, s_w, bias, device):
+    _weight(packed, s_w, 2 * n, k, device)
+    if bias is not None:
+        _tensor(bias, "bias", (2 * n,), torch.bfloat16, device)
 
 
 def sfp8_gated_linear(a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k, act="silu", bias=None,
@@ -695,25 +754,14 @@ def sfp8_gated_linear(a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k, act="silu",
     """h [m, n] bf16 = act(gate) * up of a quantised activation a_q [m, k],
     s_a [m]; packed, s_w from sfp8_prepare_gated_weight_24, bias [2n] bf16
     (gate's n values, then up's)."""
-    lib = load_library()
-    _require_cuda(a_q, s_a, packed, s_w, bias)
-    if a_q.dim() != 2:
-        raise ValueError("a_q must be 2-D")
-    m, dev = a_q.shape[0], a_q.device
-    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
-    _tensor(s_a, "s_a", (m,), torch.float32, dev)
-    _gated_args(n, k, packed, s_w, bias, dev)
-    if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
-    _tensor(out, "out", (m, n), torch.bfloat16, dev)
+    m, dev = _codes(a_q, s_a, k)
+    _gated_weight(n, k, packed, s_w, bias, dev)
+    out = _out(out, "out", (m, n), torch.bfloat16, dev)
     if workspace is None:
         workspace = new_gated_workspace(m, n, k, dev)
-    with torch.cuda.device(dev):
-        st = lib.sfp8_gated_linear(_ptr(a_q), DTYPE[_fp8_name(a_dtype)], _ptr(s_a), m,
-                                   _ptr(packed), DTYPE[_fp8_name(w_dtype)], _ptr(s_w), n, k,
-                                   _activation(act), _ptr(bias), _ptr(out), _ptr(workspace),
-                                   _ws_bytes(workspace, dev), _stream(dev))
-    _check(st, "sfp8_gated_linear")
+    _run("sfp8_gated_linear", dev, _addr(a_q), _fp8(a_dtype), _addr(s_a), m, _addr(packed),
+         _fp8(w_dtype), _addr(s_w), n, k, _activation(act), _addr(bias), _addr(out),
+         *_workspace(workspace, dev))
     return out
 
 
@@ -722,72 +770,44 @@ def sfp8_gated_linear_quant(x, a_dtype, packed, w_dtype, s_w, n, k, act="silu", 
     """Quantise x [m, k] (bf16/f16/f32, unit column stride) row-wise and apply
     the gated block, one library call: returns (h [m, n] bf16, a_q [m, k]
     uint8, s_a [m] f32); a_q and s_a are what the backward pass needs."""
-    lib = load_library()
-    _require_cuda(x, packed, s_w, bias)
-    if x.dim() != 2 or x.stride(1) != 1 or x.shape[1] != k:
-        raise ValueError("x must be [m, k=%d] with unit column stride" % k)
+    xd, ld = _rows_in(x, "x", k)
     m, dev = x.shape[0], x.device
-    xd = TORCH_WIDE.get(x.dtype)
-    if xd is None:
-        raise ValueError("x dtype must be bfloat16, float16 or float32")
-    _gated_args(n, k, packed, s_w, bias, dev)
-    if out is None:
-        out = torch.empty((m, n), dtype=torch.bfloat16, device=dev)
-    if a_q is None:
-        a_q = torch.empty((m, k), dtype=torch.uint8, device=dev)
-    if s_a is None:
-        s_a = torch.empty((m,), dtype=torch.float32, device=dev)
-    _tensor(out, "out", (m, n), torch.bfloat16, dev)
-    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
-    _tensor(s_a, "s_a", (m,), torch.float32, dev)
+    _gated_weight(n, k, packed, s_w, bias, dev)
+    out = _out(out, "out", (m, n), torch.bfloat16, dev)
+    a_q = _out(a_q, "a_q", (m, k), torch.uint8, dev)
+    s_a = _out(s_a, "s_a", (m,), torch.float32, dev)
     if workspace is None:
         workspace = new_gated_quant_workspace(m, n, k, dev)
-    ld = x.stride(0) if m > 1 else k
-    with torch.cuda.device(dev):
-        st = lib.sfp8_gated_linear_quant(_ptr(x), DTYPE[xd], ld, DTYPE[_fp8_name(a_dtype)],
-                                         _ptr(a_q), _ptr(s_a), m, _ptr(packed),
-                                         DTYPE[_fp8_name(w_dtype)], _ptr(s_w), n, k,
-                                         _activation(act), _ptr(bias), _ptr(out),
-                                         _ptr(workspace), _ws_bytes(workspace, dev),
-                                         _stream(dev))
-    _check(st, "sfp8_gated_linear_quant")
+    _run("sfp8_gated_linear_quant", dev, _addr(x), xd, ld, _fp8(a_dtype), _addr(a_q), _addr(s_a),
+         m, _addr(packed), _fp8(w_dtype), _addr(s_w), n, k, _activation(act), _addr(bias),
+         _addr(out), *_workspace(workspace, dev))
     return out, a_q, s_a
 
 
-# ---------------------------------------------------------------- backward passes
+# ---- backward passes
 
 
 def new_linear_backward_workspace(m, n, k, device):
     """A workspace for sfp8_sparse_linear_backward(m, n, k) on `device`."""
-    return _new_workspace(load_library().sfp8_sparse_linear_backward_workspace_bytes, m, n, k,
+    return _new_workspace(load_library().sfp8_sparse_linear_backward_workspace_bytes, (m, n, k),
                           device)
 
 
 def new_gated_backward_workspace(m, n, k, device):
     """A workspace for sfp8_gated_linear_backward(m, n, k) on `device`."""
-    return _new_workspace(load_library().sfp8_gated_linear_backward_workspace_bytes, m, n, k,
+    return _new_workspace(load_library().sfp8_gated_linear_backward_workspace_bytes, (m, n, k),
                           device)
 
 
-def _grad_outputs(m, rows, k, need, given, device):
-    """The gradient tensors asked for: a given one (checked), a new one, or None."""
-    out = []
-    for wanted, t, what, shape in zip(need, given, ("dx", "dw", "dbias"),
-                                      ((m, k), (rows, k), (rows,))):
-        if t is not None:
-            _tensor(t, what, shape, torch.bfloat16, device)
-        elif wanted:
-            t = torch.empty(shape, dtype=torch.bfloat16, device=device)
-        out.append(t)
-    return out
+def _gradient(t, wanted, what, shape, device):
+    """A gradient asked for: given (checked) or new; None where it is not."""
+    return _out(t, what, shape, torch.bfloat16, device) if wanted or t is not None else None
 
 
-def _grad_input(dy, what, m, n, device):
-    if (dy.dim() != 2 or tuple(dy.shape) != (m, n) or dy.dtype != torch.bfloat16
-            or dy.device != device or (n > 1 and dy.stride(1) != 1)):
-        raise ValueError("%s must be a bfloat16 tensor of shape %s with unit column stride on %s"
-                         % (what, (m, n), device))
-    return dy.stride(0) if m > 1 else n
+def _grad_in(dy, what, m, n, device):
+    if dy.shape != (m, n) or dy.dtype != torch.bfloat16 or dy.device != device:
+        raise ValueError("%s must be a bfloat16 tensor of shape %s on %s" % (what, (m, n), device))
+    return _rows_in(dy, what)[1]
 
 
 def sfp8_sparse_linear_backward(dy, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k, need_dx=True,
@@ -797,24 +817,17 @@ def sfp8_sparse_linear_backward(dy, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, 
     8-bit checkpoint a_q [m, k], s_a [m]: returns (dx [m, k], dw [n, k],
     dbias [n]), bf16, None where not asked for.  A given dx, dw or dbias is
     written (and counts as asked for)."""
-    lib = load_library()
-    _require_cuda(dy, a_q, s_a, packed, s_w)
-    if a_q.dim() != 2:
-        raise ValueError("a_q must be 2-D")
-    m, dev = a_q.shape[0], a_q.device
-    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
-    _tensor(s_a, "s_a", (m,), torch.float32, dev)
+    m, dev = _codes(a_q, s_a, k)
     _weight(packed, s_w, n, k, dev)
-    ld = _grad_input(dy, "dy", m, n, dev)
-    dx, dw, dbias = _grad_outputs(m, n, k, (need_dx, need_dw, need_dbias), (dx, dw, dbias), dev)
+    ld = _grad_in(dy, "dy", m, n, dev)
+    dx = _gradient(dx, need_dx, "dx", (m, k), dev)
+    dw = _gradient(dw, need_dw, "dw", (n, k), dev)
+    dbias = _gradient(dbias, need_dbias, "dbias", (n,), dev)
     if workspace is None:
         workspace = new_linear_backward_workspace(m, n, k, dev)
-    with torch.cuda.device(dev):
-        st = lib.sfp8_sparse_linear_backward(
-            _ptr(dy), ld, _ptr(a_q), DTYPE[_fp8_name(a_dtype)], _ptr(s_a), m, _ptr(packed),
-            DTYPE[_fp8_name(w_dtype)], _ptr(s_w), n, k, _ptr(dx), _ptr(dw), _ptr(dbias),
-            _ptr(workspace), _ws_bytes(workspace, dev), _stream(dev))
-    _check(st, "sfp8_sparse_linear_backward")
+    _run("sfp8_sparse_linear_backward", dev, _addr(dy), ld, _addr(a_q), _fp8(a_dtype),
+         _addr(s_a), m, _addr(packed), _fp8(w_dtype), _addr(s_w), n, k, _addr(dx), _addr(dw),
+         _addr(dbias), *_workspace(workspace, dev))
     return dx, dw, dbias
 
 
@@ -825,85 +838,67 @@ def sfp8_gated_linear_backward(dh, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k
     8-bit checkpoint a_q [m, k], s_a [m]: returns (dx [m, k], dw [2n, k],
     dbias [2n]), bf16, None where not asked for; dw's and dbias's first n rows
     are gate's, the others up's."""
-    lib = load_library()
-    _require_cuda(dh, a_q, s_a, packed, s_w, bias)
-    if a_q.dim() != 2:
-        raise ValueError("a_q must be 2-D")
-    m, dev = a_q.shape[0], a_q.device
-    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
-    _tensor(s_a, "s_a", (m,), torch.float32, dev)
-    _gated_args(n, k, packed, s_w, bias, dev)
-    ld = _grad_input(dh, "dh", m, n, dev)
-    dx, dw, dbias = _grad_outputs(m, 2 * n, k, (need_dx, need_dw, need_dbias), (dx, dw, dbias),
-                                  dev)
+    m, dev = _codes(a_q, s_a, k)
+    _gated_weight(n, k, packed, s_w, bias, dev)
+    ld = _grad_in(dh, "dh", m, n, dev)
+    dx = _gradient(dx, need_dx, "dx", (m, k), dev)
+    dw = _gradient(dw, need_dw, "dw", (2 * n, k), dev)
+    dbias = _gradient(dbias, need_dbias, "dbias", (2 * n,), dev)
     if workspace is None:
         workspace = new_gated_backward_workspace(m, n, k, dev)
-    with torch.cuda.device(dev):
-        st = lib.sfp8_gated_linear_backward(
-            _ptr(dh), ld, _ptr(a_q), DTYPE[_fp8_name(a_dtype)], _ptr(s_a), m, _ptr(packed),
-            DTYPE[_fp8_name(w_dtype)], _ptr(s_w), n, k, _activation(act), _ptr(bias), _ptr(dx),
-            _ptr(dw), _ptr(dbias), _ptr(workspace), _ws_bytes(workspace, dev), _stream(dev))
-    _check(st, "sfp8_gated_linear_backward")
+    _run("sfp8_gated_linear_backward", dev, _addr(dh), ld, _addr(a_q), _fp8(a_dtype), _addr(s_a),
+         m, _addr(packed), _fp8(w_dtype), _addr(s_w), n, k, _activation(act), _addr(bias),
+         _addr(dx), _addr(dw), _addr(dbias), *_workspace(workspace, dev))
     return dx, dw, dbias
 
 
-# ---------------------------------------------------------------- layer norm
+# ---- layer norm
 
 
-def _norm_input(x, what):
-    _require_cuda(x)
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError("%s must be 2-D with unit column stride" % what)
-    xd = TORCH_WIDE.get(x.dtype)
-    if xd is None:
-        raise ValueError("%s dtype must be bfloat16, float16 or float32" % what)
-    return xd, x.stride(0) if x.shape[0] > 1 else x.shape[1]
+def _norm_param(t, what, x):
+    """A weight or bias of x's dtype or float32; its dtype's code."""
+    if t is None:
+        return None
+    if t.dtype != x.dtype and t.dtype != torch.float32:
+        raise ValueError("%s must have x's dtype or float32" % what)
+    _tensor(t, what, (x.shape[1],), t.dtype, x.device)
+    return DTYPE[TORCH_WIDE[t.dtype]]
 
 
-def _norm_params(weight, bias, x):
-    """The parameters' common dtype name (x's or f32)."""
-    dtype = None
-    for t, what in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            continue
-        dtype = t.dtype if dtype is None else dtype
-        if t.dtype != dtype or t.dtype not in (x.dtype, torch.float32):
-            raise ValueError("weight and bias must both have x's dtype, or both float32")
-        _tensor(t, what, (x.shape[1],), t.dtype, x.device)
-    return TORCH_WIDE[x.dtype if dtype is None else dtype]
-
-
-def _norm_call(x, weight, bias, eps, y, q, q_dtype, scales, mean, rstd):
-    lib = load_library()
-    xd, ld = _norm_input(x, "x")
-    pd = _norm_params(weight, bias, x)
+def _norm_forward(x, weight, bias, eps, out, q, q_dtype, scales, mean, rstd):
+    xd, ld = _rows_in(x, "x")
+    pd, bd = _norm_param(weight, "weight", x), _norm_param(bias, "bias", x)
+    if pd is not None and bd is not None and pd != bd:
+        raise ValueError("weight and bias must have the same dtype")
     rows, cols = x.shape
-    for t, what, dtype, shape in ((y, "out", x.dtype, (rows, cols)),
-                                  (q, "q", torch.uint8, (rows, cols)),
-                                  (scales, "scales", torch.float32, (rows,)),
-                                  (mean, "mean", torch.float32, (rows,)),
-                                  (rstd, "rstd", torch.float32, (rows,))):
-        if t is not None:
-            _tensor(t, what, shape, dtype, x.device)
-    with torch.cuda.device(x.device):
-        st = lib.sfp8_layernorm(_ptr(x), DTYPE[xd], rows, cols, ld, _ptr(weight), _ptr(bias),
-                                DTYPE[pd], eps, _ptr(y), _ptr(q), DTYPE[_fp8_name(q_dtype)],
-                                _ptr(scales), _ptr(mean), _ptr(rstd), _stream(x.device))
-    _check(st, "sfp8_layernorm")
+    pd = pd if pd is not None else bd if bd is not None else xd
+    _run("sfp8_layernorm", x.device, _addr(x), xd, rows, cols, ld, _addr(weight), _addr(bias), pd,
+         eps, _addr(out), _addr(q), _fp8(q_dtype), _addr(scales), _addr(mean), _addr(rstd))
+
+
+def _row_vectors(rows, device, *given):
+    """float32 [rows] outputs: the given ones (name, tensor) checked, the
+    others views of one new buffer."""
+    new = [t for _, t in given if t is None]
+    if new:
+        new = list(torch.empty((len(new), rows), dtype=torch.float32, device=device).unbind())
+    out = []
+    for what, t in given:
+        if t is None:
+            t = new.pop()
+        else:
+            _tensor(t, what, (rows,), torch.float32, device)
+        out.append(t)
+    return out
 
 
 def sfp8_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, mean=None, rstd=None):
     """Layer norm of x [rows, cols] bf16/f16/f32 (unit column stride), weight
     and bias [cols] of x's dtype or float32: returns (y of x's dtype, mean
     [rows], rstd [rows] float32)."""
-    _norm_input(x, "x")
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    if mean is None:
-        mean = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
-    if rstd is None:
-        rstd = torch.empty((x.shape[0],), dtype=torch.float32, device=x.device)
-    _norm_call(x, weight, bias, eps, out, None, "e4m3", None, mean, rstd)
+    out = _out(out, "out", x.shape, x.dtype, x.device)
+    mean, rstd = _row_vectors(x.shape[0], x.device, ("mean", mean), ("rstd", rstd))
+    _norm_forward(x, weight, bias, eps, out, None, "e4m3", None, mean, rstd)
     return out, mean, rstd
 
 
@@ -912,25 +907,19 @@ def sfp8_layernorm_quant(x, weight=None, bias=None, eps=1e-5, q_dtype="e4m3", q=
     """Layer norm of x straight to row-wise FP8 codes, the input of the linear
     and the gated block: returns (q [rows, cols] uint8, scales, mean, rstd
     [rows] float32).  A given `out` also receives y in x's dtype."""
-    _norm_input(x, "x")
-    rows = x.shape[0]
-    if q is None:
-        q = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-    if scales is None:
-        scales = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    if mean is None:
-        mean = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    if rstd is None:
-        rstd = torch.empty((rows,), dtype=torch.float32, device=x.device)
-    _norm_call(x, weight, bias, eps, out, q, q_dtype, scales, mean, rstd)
+    q = _out(q, "q", x.shape, torch.uint8, x.device)
+    if out is not None:
+        _tensor(out, "out", x.shape, x.dtype, x.device)
+    scales, mean, rstd = _row_vectors(x.shape[0], x.device, ("scales", scales), ("mean", mean),
+                                      ("rstd", rstd))
+    _norm_forward(x, weight, bias, eps, out, q, q_dtype, scales, mean, rstd)
     return q, scales, mean, rstd
 
 
 def new_layernorm_backward_workspace(rows, cols, device):
     """A workspace for sfp8_layernorm_backward on `device`."""
-    with torch.cuda.device(device):
-        nbytes = int(load_library().sfp8_layernorm_backward_workspace_bytes(rows, cols))
-    return torch.empty((max(nbytes, 16),), dtype=torch.uint8, device=device)
+    return _new_workspace(load_library().sfp8_layernorm_backward_workspace_bytes, (rows, cols),
+                          device)
 
 
 def sfp8_layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None,
@@ -938,33 +927,23 @@ def sfp8_layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, db
     """Gradients of layer norm from dy [rows, cols] (x's dtype) and the
     forward's x, weight (or None), mean and rstd: returns (dx of x's dtype,
     dweight, dbias [cols] float32)."""
-    lib = load_library()
-    xd, ld_x = _norm_input(x, "x")
-    dyd, ld_dy = _norm_input(dy, "dy")
-    if dyd != xd or dy.shape != x.shape or dy.device != x.device:
-        raise ValueError("dy must have x's shape, dtype and device")
-    pd = _norm_params(weight, None, x)
-    rows, cols = x.shape
+    xd, ld_x = _rows_in(x, "x")
+    dyd, ld_dy = _rows_in(dy, "dy")
     dev = x.device
+    if dyd != xd or dy.shape != x.shape or dy.device != dev:
+        raise ValueError("dy must have x's shape, dtype and device")
+    pd = _norm_param(weight, "weight", x)
+    rows, cols = x.shape
     _tensor(mean, "mean", (rows,), torch.float32, dev)
     _tensor(rstd, "rstd", (rows,), torch.float32, dev)
-    if dx is None:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    if dweight is None:
-        dweight = torch.empty((cols,), dtype=torch.float32, device=dev)
-    if dbias is None:
-        dbias = torch.empty((cols,), dtype=torch.float32, device=dev)
-    _tensor(dx, "dx", (rows, cols), x.dtype, dev)
-    _tensor(dweight, "dweight", (cols,), torch.float32, dev)
-    _tensor(dbias, "dbias", (cols,), torch.float32, dev)
+    dx = _out(dx, "dx", (rows, cols), x.dtype, dev)
+    dweight = _out(dweight, "dweight", (cols,), torch.float32, dev)
+    dbias = _out(dbias, "dbias", (cols,), torch.float32, dev)
     if workspace is None:
         workspace = new_layernorm_backward_workspace(rows, cols, dev)
-    with torch.cuda.device(dev):
-        st = lib.sfp8_layernorm_backward(
-            _ptr(dy), ld_dy, _ptr(x), DTYPE[xd], rows, cols, ld_x, _ptr(weight), DTYPE[pd],
-            _ptr(mean), _ptr(rstd), _ptr(dx), _ptr(dweight), _ptr(dbias), _ptr(workspace),
-            _ws_bytes(workspace, dev), _stream(dev))
-    _check(st, "sfp8_layernorm_backward")
+    _run("sfp8_layernorm_backward", dev, _addr(dy), ld_dy, _addr(x), xd, rows, cols, ld_x,
+         _addr(weight), xd if pd is None else pd, _addr(mean), _addr(rstd), _addr(dx),
+         _addr(dweight), _addr(dbias), *_workspace(workspace, dev))
     return dx, dweight, dbias
 
 

@@ -10,51 +10,87 @@ namespace {
 
 // ------------------------------------------------------------------ gradient GEMM plan
 
+// One product's split into work items.
 struct GradPlan {
-  int bn;
   int splits;
   int m_tiles, n_tiles;
   int stages;             // of 64 along the contraction
+  int items;
   size_t partial_bytes;   // fp32 partial sums (splits > 1)
 };
 
-// Tile width and contraction splits that finish first by this estimate, in
-// units of one 64-deep stage of a 256-wide tile (about 0.3 us): every round
-// of work items takes its stages -- a 128-wide tile's stage costs 0.6 of a
-// 256-wide one's, not half, since A's share of the loads stays -- plus 6
-// for filling the pipeline and storing the last tile, and splitting adds a launch
-// and the round trip of the partial sums (write and read, 4 bytes each, at
-// about 5 TB/s).
-GradPlan grad_plan(int64_t rows, int64_t cols, int64_t contraction, int num_sms) {
-  GradPlan best{};
+struct GradPlans {
+  int bn;                 // tile width of both
+  int first;              // which product's items come first (the longer ones)
+  int lag_rounds;         // see GgWalk
+  GradPlan p[2];          // dx, dw
+};
+
+constexpr int kGradMinStages = 8;   // an item's epilogue takes about as long as 8 stages
+
+GradPlan grad_split(int64_t rows, int64_t cols, int64_t contraction, int bn, int splits) {
+  GradPlan g{};
+  g.splits = splits;
+  g.m_tiles = static_cast<int>((rows + kGgTileM - 1) / kGgTileM);
+  g.n_tiles = static_cast<int>((cols + bn - 1) / bn);
+  g.stages = static_cast<int>((contraction + kGgStageK - 1) / kGgStageK);
+  g.items = g.m_tiles * g.n_tiles * splits;
+  g.partial_bytes = splits > 1 ? static_cast<size_t>(splits) * static_cast<size_t>(rows) *
+                                     static_cast<size_t>(cols) * sizeof(float)
+                               : 0;
+  return g;
+}
+
+// Tile width and splits that finish first by this estimate, in units of one
+// 64-deep stage of a 256-wide tile (about 0.3 us): the busiest pair's stages
+// by GgWalk's order (a 128-wide tile's stage costs 0.6 of a 256-wide one's,
+// not half, since A's share of the loads stays), plus, where a contraction is
+// split, a launch (10) and the round trip of the partial sums (4 bytes
+// written and read at about 5 TB/s).  Contractions are split only as far as
+// two items a pair.  A call for one of the two gradients uses the same split.
+GradPlans grad_plan(int64_t m, int64_t rows, int64_t k, int num_sms) {
+  GradPlans best{};
   double best_cost = 0.0;
-  const int64_t pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
-  const int stages = static_cast<int>((contraction + kGgStageK - 1) / kGgStageK);
+  const int pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
+  static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32};
   for (int bn : {256, 128}) {
-    const int64_t mt = (rows + kGgTileM - 1) / kGgTileM;
-    const int64_t nt = (cols + bn - 1) / bn;
-    for (int splits = 1; splits <= 32; ++splits) {
-      // at least 8 stages a split
-      if (splits > 1 && stages / splits < 8) break;
-      const int64_t rounds = (mt * nt * splits + pairs - 1) / pairs;
-      const double stage = bn == 256 ? 1.0 : 0.6;
-      double cost = static_cast<double>(rounds) * ((stages + splits - 1) / splits * stage) + 6.0;
-      if (splits > 1)
-        cost += 10.0 + 8.0 * static_cast<double>(rows) * static_cast<double>(cols) * splits / 1.5e6;
-      if (best.bn == 0 || cost < best_cost) {
-        best_cost = cost;
-        best.bn = bn;
-        best.splits = splits;
-        best.m_tiles = static_cast<int>(mt);
-        best.n_tiles = static_cast<int>(nt);
+    const double stage = bn == 256 ? 1.0 : 0.6;
+    for (int s0 : kSplits) {
+      const GradPlan g0 = grad_split(m, k, rows, bn, s0);
+      if (s0 > 1 && (g0.stages / s0 < kGradMinStages || g0.items > 2 * pairs)) break;
+      for (int s1 : kSplits) {
+        const GradPlan g1 = grad_split(rows, k, m, bn, s1);
+        if (s1 > 1 && (g1.stages / s1 < kGradMinStages || g1.items > 2 * pairs)) break;
+        // stages an item, longer ones first
+        double u[2] = {static_cast<double>((g0.stages + s0 - 1) / s0),
+                       static_cast<double>((g1.stages + s1 - 1) / s1)};
+        const int64_t n[2] = {g0.items, g1.items};
+        for (double& v : u) v = v < kGradMinStages ? kGradMinStages : v;
+        const int first = u[1] > u[0] ? 1 : 0;
+        const double ua = u[first], ub = u[first ^ 1];
+        const int64_t na = n[first], nb = n[first ^ 1];
+        const int64_t q = na % pairs, lag = q == 0 ? 0 : pairs - q;
+        const int64_t lag_rounds = static_cast<int64_t>(ua / ub + 0.5);
+        const int64_t lag_items = lag * lag_rounds < nb ? lag * lag_rounds : nb;
+        const double rest = static_cast<double>((nb - lag_items + pairs - 1) / pairs) * ub;
+        const double full = static_cast<double>((na + pairs - 1) / pairs) * ua;
+        const double less = static_cast<double>(na / pairs) * ua +
+                            (lag > 0 ? static_cast<double>((lag_items + lag - 1) / lag) * ub : 0.0);
+        double cost = ((full > less ? full : less) + rest) * stage + 6.0;
+        if (s0 > 1 || s1 > 1) cost += 10.0;
+        if (s0 > 1) cost += static_cast<double>(g0.partial_bytes) * 2 / 1.5e6;
+        if (s1 > 1) cost += static_cast<double>(g1.partial_bytes) * 2 / 1.5e6;
+        if (best.bn == 0 || cost < best_cost) {
+          best_cost = cost;
+          best.bn = bn;
+          best.first = first;
+          best.lag_rounds = static_cast<int>(lag_rounds);
+          best.p[0] = g0;
+          best.p[1] = g1;
+        }
       }
     }
   }
-  best.stages = stages;
-  best.partial_bytes = best.splits > 1 ? static_cast<size_t>(best.splits) *
-                                             static_cast<size_t>(rows) *
-                                             static_cast<size_t>(cols) * sizeof(float)
-                                       : 0;
   return best;
 }
 
@@ -75,11 +111,10 @@ sfp8_status encode_bf16_2d(CUtensorMap* map, const void* base, uint64_t inner, u
   return r == CUDA_SUCCESS ? SFP8_OK : SFP8_ERR_CUDA;
 }
 
-template <int BN, bool A_MN>
-sfp8_status launch_grad_gemm_cfg(DeviceInfo* dev, const CUtensorMap& ta, const CUtensorMap& tb,
-                                 GgParams prm, cudaStream_t st) {
-  auto kern = grad_gemm_kernel<BN, A_MN>;
-  constexpr int slot = (BN == 256 ? 0 : 2) + (A_MN ? 1 : 0);
+template <int BN>
+sfp8_status launch_grad_gemm(DeviceInfo* dev, const GgMaps& maps, GgParams prm, cudaStream_t st) {
+  auto kern = grad_gemm_kernel<BN>;
+  constexpr int slot = BN == 256 ? 0 : 1;
   constexpr int smem = GgCfg<BN>::kSmemBytes;
   static_assert(smem <= kSmemLimit, "shared memory of the gradient GEMM");
   {
@@ -107,97 +142,60 @@ sfp8_status launch_grad_gemm_cfg(DeviceInfo* dev, const CUtensorMap& ta, const C
       dev->grad_clusters[slot] = clusters;
     }
   }
-  prm.pairs = prm.items < dev->grad_clusters[slot] ? prm.items : dev->grad_clusters[slot];
-  prm.idesc = make_idesc_bf16(A_MN, true, kGgTileM, BN);
-  return launch_dependent(kern, dim3(2 * prm.pairs), dim3(kGgThreads), smem, st, ta, tb, prm);
+  const int items = prm.prob[0].items + prm.prob[1].items;
+  prm.pairs = items < dev->grad_clusters[slot] ? items : dev->grad_clusters[slot];
+  return launch_dependent(kern, dim3(2 * prm.pairs), dim3(kGgThreads), smem, st, maps, prm);
 }
 
-unsigned grid_for(int64_t items, int per_block, const DeviceInfo* dev, int blocks_per_sm) {
+int blocks_for(int64_t items, int per_block, const DeviceInfo* dev, int blocks_per_sm) {
   int64_t b = (items + per_block - 1) / per_block;
   const int64_t cap = static_cast<int64_t>(dev->num_sms) * blocks_per_sm;
   if (b > cap) b = cap;
-  return static_cast<unsigned>(b < 1 ? 1 : b);
-}
-
-// D [rows, cols] = sum over t < contraction of A[r, t] B[t, c].  A is
-// [rows][lda] (a_mn false) or [contraction][lda] (a_mn true), B is
-// [contraction][cols]; row_scale [rows] is divided out of D (or null).
-sfp8_status launch_grad_gemm(DeviceInfo* dev, const GradPlan& pl, const void* a, int64_t lda,
-                             bool a_mn, const void* b, int64_t rows, int64_t cols,
-                             int64_t contraction, const float* row_scale, void* d,
-                             int64_t pair_rows, float* partial, cudaStream_t st) {
-  CUtensorMap ta, tb;
-  sfp8_status s = a_mn ? encode_bf16_2d(&ta, a, rows, contraction, lda, kGgStageK)
-                       : encode_bf16_2d(&ta, a, contraction, rows, lda, 128);
-  if (s != SFP8_OK) return s;
-  s = encode_bf16_2d(&tb, b, cols, contraction, cols, kGgStageK);
-  if (s != SFP8_OK) return s;
-  GgParams prm{};
-  prm.d = static_cast<__nv_bfloat16*>(d);
-  prm.partial = partial;
-  prm.ld_d = cols;
-  prm.rows = static_cast<int>(rows);
-  prm.cols = static_cast<int>(cols);
-  prm.m_tiles = pl.m_tiles;
-  prm.n_tiles = pl.n_tiles;
-  prm.stages_total = pl.stages;
-  prm.splits = pl.splits;
-  prm.items = pl.m_tiles * pl.n_tiles * pl.splits;
-  // about as many row tiles as column tiles in flight at a time
-  prm.band = 8;
-  prm.row_scale = row_scale;
-  prm.pair_rows = static_cast<int>(pair_rows);
-  if (pl.bn == 256)
-    s = a_mn ? launch_grad_gemm_cfg<256, true>(dev, ta, tb, prm, st)
-             : launch_grad_gemm_cfg<256, false>(dev, ta, tb, prm, st);
-  else
-    s = a_mn ? launch_grad_gemm_cfg<128, true>(dev, ta, tb, prm, st)
-             : launch_grad_gemm_cfg<128, false>(dev, ta, tb, prm, st);
-  if (s != SFP8_OK || pl.splits == 1) return s;
-  return launch_dependent(grad_gemm_join_kernel, dim3(grid_for(rows * (cols / 8), 256, dev, 8)),
-                          dim3(256), 0, st, static_cast<const float*>(partial), pl.splits,
-                          static_cast<int>(rows), static_cast<int>(cols), row_scale,
-                          static_cast<__nv_bfloat16*>(d), static_cast<long long>(cols),
-                          static_cast<int>(pair_rows));
+  return static_cast<int>(b);
 }
 
 // ------------------------------------------------------------------ backward plan
 
 // Workspace of a backward pass over `rows` weight rows (2n for a gated block),
-// in this order, every part on a 256-byte boundary.
+// every part on a 256-byte boundary.  It is sized for all three gradients, so
+// that one query serves every call of the sizes.
 struct BackwardPlan {
+  GradPlans grads;
   int64_t ld_dz;          // row stride of dz in the workspace (a multiple of 8)
-  GradPlan dx, dw;
-  int runs;               // row runs of the column sums
-  size_t dz_off, expand_off, partial_off, sums_off, total;
+  int runs;               // rows of the column sums
+  size_t dz_off, what_off, xhat_off, partial_off, sums_off, total;
 };
 
 constexpr int64_t kColSumMinRows = 64;   // rows a run at least
 
-BackwardPlan backward_plan(int64_t m, int64_t rows, int64_t k, bool keep_dz, int num_sms) {
+size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
+
+// sum_runs: rows of column sums that the gated gradient epilogue writes, or 0:
+// as many runs as fill the device.
+BackwardPlan backward_plan(int64_t m, int64_t rows, int64_t k, bool keep_dz, int sum_runs,
+                           int num_sms) {
   BackwardPlan b{};
-  auto up = [](size_t v) { return (v + 255) & ~static_cast<size_t>(255); };
   b.ld_dz = (rows + 7) / 8 * 8;
-  b.dx = grad_plan(m, k, rows, num_sms);
-  b.dw = grad_plan(rows, k, m, num_sms);
-  // enough blocks of column sums to fill the device, with long enough runs
-  const int64_t cols = (rows + kColSumCols - 1) / kColSumCols;
-  int64_t runs = (static_cast<int64_t>(num_sms) * 8 + cols - 1) / cols;
-  if (runs > (m + kColSumMinRows - 1) / kColSumMinRows)
-    runs = (m + kColSumMinRows - 1) / kColSumMinRows;
-  b.runs = static_cast<int>(runs < 1 ? 1 : runs);
+  b.runs = sum_runs;
+  if (sum_runs == 0) {
+    const int64_t cols = (rows + kColSumCols - 1) / kColSumCols;
+    int64_t runs = (static_cast<int64_t>(num_sms) * 4 + cols - 1) / cols;
+    const int64_t most = (m + kColSumMinRows - 1) / kColSumMinRows;
+    if (runs > most) runs = most;
+    b.runs = static_cast<int>(runs < 1 ? 1 : runs);
+  }
   size_t at = 0;
   b.dz_off = at;
-  if (keep_dz) at = up(at + static_cast<size_t>(m) * static_cast<size_t>(b.ld_dz) * 2);
-  // the expanded weight, then (the input gradient done) the expanded checkpoint
-  b.expand_off = at;
-  at = up(at + static_cast<size_t>(rows > m ? rows : m) * static_cast<size_t>(k) * 2);
-  b.partial_off = at;
-  at = up(at + (b.dx.partial_bytes > b.dw.partial_bytes ? b.dx.partial_bytes
-                                                        : b.dw.partial_bytes));
+  if (keep_dz) at = up256(at + static_cast<size_t>(m) * static_cast<size_t>(b.ld_dz) * 2);
+  b.what_off = at;
+  at = up256(at + static_cast<size_t>(rows) * static_cast<size_t>(k) * 2);
+  b.xhat_off = at;
+  at = up256(at + static_cast<size_t>(m) * static_cast<size_t>(k) * 2);
   b.sums_off = at;
-  at = up(at + static_cast<size_t>(b.runs) * static_cast<size_t>(rows) * sizeof(float));
-  b.total = at;
+  at = up256(at + static_cast<size_t>(b.runs) * static_cast<size_t>(rows) * sizeof(float));
+  b.partial_off = at;
+  b.grads = grad_plan(m, rows, k, num_sms);
+  b.total = at + up256(b.grads.p[0].partial_bytes) + up256(b.grads.p[1].partial_bytes);
   return b;
 }
 
@@ -220,57 +218,110 @@ struct BackwardCall {
   void* dbias;
 };
 
-// dx, dw and dbias from dz [m, rows] (row stride ld, 16-byte aligned, ld a
-// multiple of 8): expand the weight, dx; expand the checkpoint, dw; column
-// sums.  pair_rows: n for a gated block (dz then holds both scales, dw and
-// dbias leave in gate-then-up order), else 0.
+// The expanded operands of the gradients asked for (and, for a plain linear,
+// the copy and the column sums of dy), in one launch.  scaled: with the scales
+// multiplied in.
+sfp8_status launch_prologue(DeviceInfo* dev, const BackwardPlan& bp, const BackwardCall& c,
+                            bool scaled, const void* dy, int64_t ld_dy, bool copy, bool sums,
+                            uint8_t* ws, cudaStream_t st) {
+  PrologueParams p{};
+  p.packed = static_cast<const uint8_t*>(c.packed);
+  p.s_w = scaled ? c.s_w : nullptr;
+  p.w_fmt = c.w_dtype;
+  p.rows = c.rows;
+  p.k = c.k;
+  p.what = reinterpret_cast<__nv_bfloat16*>(ws + bp.what_off);
+  p.a_q = static_cast<const uint8_t*>(c.a_q);
+  p.s_a = scaled ? c.s_a : nullptr;
+  p.a_fmt = c.a_dtype;
+  p.m = c.m;
+  p.xhat = reinterpret_cast<__nv_bfloat16*>(ws + bp.xhat_off);
+  p.dy = static_cast<const __nv_bfloat16*>(dy);
+  p.ld_dy = ld_dy;
+  p.copy = reinterpret_cast<__nv_bfloat16*>(ws + bp.dz_off);
+  p.ld_copy = bp.ld_dz;
+  p.sums = reinterpret_cast<float*>(ws + bp.sums_off);
+  p.runs = bp.runs;
+  p.sums_by_16 = aligned(dy, 16) && ld_dy % 8 == 0;
+  if (c.dx != nullptr) p.blocks[0] = blocks_for((c.rows + 127) / 128 * (c.k / 128), 1, dev, 8);
+  if (c.dw != nullptr) p.blocks[1] = blocks_for((c.m + 127) / 128 * (c.k / 128), 1, dev, 8);
+  if (copy) p.blocks[2] = blocks_for(c.m, 1, dev, 8);
+  if (sums)
+    p.blocks[3] = static_cast<int>((c.rows + kColSumCols - 1) / kColSumCols) * bp.runs;
+  const int64_t blocks = static_cast<int64_t>(p.blocks[0]) + p.blocks[1] + p.blocks[2] +
+                         p.blocks[3];
+  if (blocks == 0) return SFP8_OK;
+  return launch_dependent(backward_prologue_kernel, dim3(static_cast<unsigned>(blocks)),
+                          dim3(256), 0, st, p);
+}
+
+// dx and dw from dz [m, rows] (row stride ld, 16-byte aligned, ld a multiple
+// of 8) and the expanded operands, one launch for both products; then the
+// join of split contractions and of the column sums.  pair_rows: n for a
+// gated block (dz then holds both scales, dw and dbias leave in gate-then-up
+// order), else 0.
 sfp8_status launch_linear_grads(DeviceInfo* dev, const BackwardPlan& bp, const BackwardCall& c,
                                 const void* dz, int64_t ld, int64_t pair_rows, uint8_t* ws,
                                 cudaStream_t st) {
-  __nv_bfloat16* expanded = reinterpret_cast<__nv_bfloat16*>(ws + bp.expand_off);
-  float* partial = reinterpret_cast<float*>(ws + bp.partial_off);
-  sfp8_status s = SFP8_OK;
-  // the scales are in the expanded operand, or in dz and divided out
-  const bool scaled_dz = pair_rows != 0;
-  const float* none = nullptr;
-  if (c.dx != nullptr) {
-    auto kern = c.w_dtype == SFP8_E5M2 ? expand_weight_kernel<SFP8_E5M2>
-                                       : expand_weight_kernel<SFP8_E4M3>;
-    s = launch_dependent(kern, dim3(grid_for(c.rows * (c.k / 32), 256, dev, 8)), dim3(256), 0, st,
-                         static_cast<const uint8_t*>(c.packed), scaled_dz ? none : c.s_w,
-                         static_cast<long long>(c.rows), static_cast<long long>(c.k), expanded);
-    if (s != SFP8_OK) return s;
-    s = launch_grad_gemm(dev, bp.dx, dz, ld, false, expanded, c.m, c.k, c.rows,
-                         scaled_dz ? c.s_a : none, c.dx, 0, partial, st);
+  const bool want[2] = {c.dx != nullptr, c.dw != nullptr};
+  JoinParams jp{};
+  if (want[0] || want[1]) {
+    const GradPlans& g = bp.grads;
+    GgParams prm{};
+    GgMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    size_t partial = bp.partial_off;
+    for (int i = 0; i < 2; ++i) {
+      if (!want[i]) continue;
+      // the longer items first; a lone product is the first
+      const int at = i == g.first || !want[1 - i] ? 0 : 1;
+      const GradPlan& pl = g.p[i];
+      GgProblem& pr = prm.prob[at];
+      const int64_t d_rows = i == 0 ? c.m : c.rows;
+      const int64_t contraction = i == 0 ? c.rows : c.m;
+      const void* b = ws + (i == 0 ? bp.what_off : bp.xhat_off);
+      sfp8_status s = i == 0 ? encode_bf16_2d(&maps.a[at], dz, c.rows, c.m, ld, 128)
+                             : encode_bf16_2d(&maps.a[at], dz, c.rows, c.m, ld, kGgStageK);
+      if (s != SFP8_OK) return s;
+      s = encode_bf16_2d(&maps.b[at], b, c.k, contraction, c.k, kGgStageK);
+      if (s != SFP8_OK) return s;
+      pr.d = static_cast<__nv_bfloat16*>(i == 0 ? c.dx : c.dw);
+      pr.partial = reinterpret_cast<float*>(ws + partial);
+      partial += up256(pl.partial_bytes);
+      pr.row_scale = pair_rows == 0 ? nullptr : i == 0 ? c.s_a : c.s_w;
+      pr.rows = static_cast<int>(d_rows);
+      pr.cols = static_cast<int>(c.k);
+      pr.m_tiles = pl.m_tiles;
+      pr.n_tiles = pl.n_tiles;
+      pr.stages_total = pl.stages;
+      pr.splits = pl.splits;
+      pr.items = pl.items;
+      pr.band = 8;   // about as many row tiles as column tiles in flight at a time
+      pr.pair_rows = i == 0 ? 0 : static_cast<int>(pair_rows);
+      pr.a_mn = i;
+      pr.idesc = make_idesc_bf16(i == 1, true, kGgTileM, static_cast<uint32_t>(g.bn));
+      if (pl.splits > 1) {
+        jp.prob[at] = pr;
+        jp.blocks[at] = blocks_for(d_rows, 16, dev, 8);
+      }
+    }
+    prm.lag_rounds = g.lag_rounds;
+    const sfp8_status s = g.bn == 256 ? launch_grad_gemm<256>(dev, maps, prm, st)
+                                      : launch_grad_gemm<128>(dev, maps, prm, st);
     if (s != SFP8_OK) return s;
   }
-  if (c.dw != nullptr) {
-    auto kern = c.a_dtype == SFP8_E5M2 ? expand_rows_kernel<SFP8_E5M2>
-                                       : expand_rows_kernel<SFP8_E4M3>;
-    s = launch_dependent(kern, dim3(grid_for(c.m * (c.k / 16), 256, dev, 8)), dim3(256), 0, st,
-                         static_cast<const uint8_t*>(c.a_q), scaled_dz ? none : c.s_a,
-                         static_cast<long long>(c.m), static_cast<long long>(c.k), expanded);
-    if (s != SFP8_OK) return s;
-    s = launch_grad_gemm(dev, bp.dw, dz, ld, true, expanded, c.rows, c.k, c.m,
-                         scaled_dz ? c.s_w : none, c.dw, pair_rows, partial, st);
-    if (s != SFP8_OK) return s;
-  }
+  int blocks = jp.blocks[0] + jp.blocks[1];
   if (c.dbias != nullptr) {
-    float* sums = reinterpret_cast<float*>(ws + bp.sums_off);
-    s = launch_dependent(column_sums_kernel,
-                         dim3(static_cast<unsigned>((c.rows + kColSumCols - 1) / kColSumCols),
-                              static_cast<unsigned>(bp.runs)),
-                         dim3(256), 0, st, static_cast<const __nv_bfloat16*>(dz),
-                         static_cast<long long>(c.m), static_cast<long long>(c.rows),
-                         static_cast<long long>(ld), scaled_dz ? c.s_a : none, sums);
-    if (s != SFP8_OK) return s;
-    s = launch_dependent(column_sums_join_kernel,
-                         dim3(static_cast<unsigned>((c.rows + 255) / 256)), dim3(256), 0, st,
-                         static_cast<const float*>(sums), bp.runs, static_cast<long long>(c.rows),
-                         scaled_dz ? c.s_w : none, static_cast<__nv_bfloat16*>(c.dbias),
-                         static_cast<long long>(pair_rows));
+    jp.sums = reinterpret_cast<const float*>(ws + bp.sums_off);
+    jp.dbias = static_cast<__nv_bfloat16*>(c.dbias);
+    jp.runs = bp.runs;
+    jp.cols = static_cast<int>(c.rows);
+    jp.pair_rows = static_cast<int>(pair_rows);
+    blocks += static_cast<int>((c.rows + 31) / 32);
   }
-  return s;
+  if (blocks == 0) return SFP8_OK;
+  return launch_dependent(backward_join_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                          st, jp);
 }
 
 // Gradients of an empty problem: no tokens or no weight rows.
@@ -328,6 +379,15 @@ LinearChoice gated_grad_choice(int64_t m, int64_t rows, int64_t k, int num_sms) 
   return c;
 }
 
+// Rows of column sums that its epilogue writes: one per token tile and warp of
+// a lane quadrant.
+int gated_grad_runs(int64_t m, int64_t rows, int64_t k, int num_sms) {
+  const LinearChoice c = gated_grad_choice(m, rows, k, num_sms);
+  const int parts = c.wt == 2 ? PairCfg<1, 2, kEpiGatedGrad>::kEpiParts
+                              : PairCfg<1, 1, kEpiGatedGrad>::kEpiParts;
+  return static_cast<int>((m + c.bn - 1) / c.bn) * parts;
+}
+
 }  // namespace
 }  // namespace sfp8
 
@@ -339,7 +399,7 @@ size_t sfp8_sparse_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
-  return backward_plan(m, n, k, n % 8 != 0, sms).total;
+  return backward_plan(m, n, k, n % 8 != 0, 0, sms).total;
 }
 
 sfp8_status sfp8_sparse_linear_backward(const void* dy, int64_t ld_dy, const void* a_q,
@@ -360,23 +420,15 @@ sfp8_status sfp8_sparse_linear_backward(const void* dy, int64_t ld_dy, const voi
   DeviceInfo* dev = nullptr;
   s = current_device(&dev);
   if (s != SFP8_OK) return s;
-  const BackwardPlan bp = backward_plan(m, n, k, n % 8 != 0, dev->num_sms);
+  const BackwardPlan bp = backward_plan(m, n, k, n % 8 != 0, 0, dev->num_sms);
   if (workspace == nullptr || workspace_bytes < bp.total) return SFP8_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return SFP8_ERR_MISALIGNED;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const void* dz = dy;
-  int64_t ld = ld_dy;
-  if (!in_place && (dx != nullptr || dw != nullptr)) {
-    dz = ws + bp.dz_off;
-    ld = bp.ld_dz;
-    s = launch_dependent(copy_rows_kernel, dim3(grid_for(m * ld, 256, dev, 8)), dim3(256), 0, st,
-                         static_cast<const __nv_bfloat16*>(dy), static_cast<long long>(m),
-                         static_cast<long long>(n), static_cast<long long>(ld_dy),
-                         reinterpret_cast<__nv_bfloat16*>(ws + bp.dz_off),
-                         static_cast<long long>(ld));
-    if (s != SFP8_OK) return s;
-  }
-  return launch_linear_grads(dev, bp, c, dz, ld, 0, ws, st);
+  const bool copy = !in_place && (dx != nullptr || dw != nullptr);
+  s = launch_prologue(dev, bp, c, true, dy, ld_dy, copy, dbias != nullptr, ws, st);
+  if (s != SFP8_OK) return s;
+  return launch_linear_grads(dev, bp, c, copy ? ws + bp.dz_off : dy, copy ? bp.ld_dz : ld_dy, 0,
+                             ws, st);
 }
 
 size_t sfp8_gated_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k) {
@@ -386,7 +438,7 @@ size_t sfp8_gated_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t 
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
-  return backward_plan(m, rows, k, true, sms).total;
+  return backward_plan(m, rows, k, true, gated_grad_runs(m, rows, k, sms), sms).total;
 }
 
 sfp8_status sfp8_gated_linear_backward(const void* dh, int64_t ld_dh, const void* a_q,
@@ -408,13 +460,18 @@ sfp8_status sfp8_gated_linear_backward(const void* dh, int64_t ld_dh, const void
   DeviceInfo* dev = nullptr;
   s = current_device(&dev);
   if (s != SFP8_OK) return s;
-  const BackwardPlan bp = backward_plan(m, rows, k, true, dev->num_sms);
+  const BackwardPlan bp = backward_plan(
+      m, rows, k, true, gated_grad_runs(m, rows, k, dev->num_sms), dev->num_sms);
   if (workspace == nullptr || workspace_bytes < bp.total) return SFP8_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return SFP8_ERR_MISALIGNED;
+  if (dx == nullptr && dw == nullptr && dbias == nullptr) return SFP8_OK;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
+  s = launch_prologue(dev, bp, c, false, nullptr, 0, false, false, ws, st);
+  if (s != SFP8_OK) return s;
   const LinearPlan pl =
       plan_from_choice(m, rows, k, dev->num_sms, gated_grad_choice(m, rows, k, dev->num_sms));
-  const GatedCall gc{kEpiGatedGrad, act, dh, ld_dh, bp.ld_dz};
+  const GatedCall gc{kEpiGatedGrad, act, dh, ld_dh, bp.ld_dz,
+                     dbias != nullptr ? reinterpret_cast<float*>(ws + bp.sums_off) : nullptr};
   s = launch_pair(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, rows, k, bias,
                   ws + bp.dz_off, st, &gc);
   if (s != SFP8_OK) return s;

@@ -26,10 +26,19 @@
 // 0 issues the MMAs, warps 5-12 are the epilogue (two per tensor-memory lane
 // quadrant, each taking every other 32-column chunk).
 //
+// One launch does both products: their tiles are one list of work items for
+// the resident CTA pairs (GgWalk), the product with the longer items first and
+// the other's filling up what that leaves uneven.  Of 128 + 256 items of 64
+// and 32 stages (m = 2048, n = k = 4096) the busiest of 74 pairs gets 224
+// stages where two launches take 256.
+//
 // Few tiles and a long contraction: it is cut into `splits` equal runs of
 // stages, every run a work item of its own that writes fp32 partial sums, and
-// a second kernel adds the runs in order (no atomics: the same bits every
+// the join kernel adds the runs in order (no atomics: the same bits every
 // time) and rounds.
+//
+// The prologue kernel expands the operands (and copies or sums dy where that
+// is needed), all in one launch of independent blocks.
 //
 // Rows and columns past the operands' ends are filled with zeros by TMA and
 // never stored.  Every wait is bounded (device_common.cuh).
@@ -64,20 +73,30 @@ struct GgCfg {
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 1024;
 };
 
-struct GgParams {
-  __nv_bfloat16* d;       // [rows][ld_d]
+// One of the two products.
+struct GgProblem {
+  __nv_bfloat16* d;       // [rows][cols]
   float* partial;         // [splits][rows][cols] fp32 (splits > 1)
-  long long ld_d;
+  const float* row_scale; // [rows], divided out of D's rows; or null
   int rows, cols;         // of D; cols a multiple of 16
   int m_tiles, n_tiles;
   int stages_total;       // ceil(contraction / 64)
   int splits;
   int items;              // m_tiles * n_tiles * splits
-  int pairs;              // gridDim.x / 2
   int band;               // row tiles per band of the tile order
-  const float* row_scale; // [rows], divided out of D's rows; or null
   int pair_rows;          // != 0: D's row r is stored at row (r & 1) * pair_rows + r / 2
+  int a_mn;               // A is MN-major
   uint32_t idesc;
+};
+
+struct GgParams {
+  GgProblem prob[2];
+  int pairs;              // gridDim.x / 2
+  int lag_rounds;         // items of product 1 that each less loaded pair takes first
+};
+
+struct GgMaps {
+  CUtensorMap a[2], b[2];
 };
 
 // Instruction descriptor of kind::f16 with bf16 operands and fp32
@@ -110,11 +129,56 @@ __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const void* desc,
       : "memory");
 }
 
-// Work item -> (row tile, column tile, split).  Items run in bands of
-// p.band row tiles, the split outermost and the row tile fastest, so that
-// the items in flight at a time form a block of D about as tall as wide and
-// share the operand stages they read through L2.
-__device__ __forceinline__ void gg_item(const GgParams& p, int i, int& mt, int& nt, int& sp) {
+// The work items of one pair, in order: product 0's items pair, pair + P, ...;
+// then, if that gave this pair one item less than others, lag_rounds items of
+// product 1; then an even share of product 1's other items.  All roles walk
+// it identically.
+struct GgWalk {
+  int pair, pairs, i, lag, lag_pairs, lag_items, phase;
+  __device__ GgWalk(const GgParams& p, int pr) : pair(pr), pairs(p.pairs), i(pr), phase(0) {
+    const int q = p.prob[0].items % pairs;
+    lag_pairs = q == 0 ? 0 : pairs - q;
+    lag = pr - q;                       // its place among the less loaded pairs
+    const int most = lag_pairs * p.lag_rounds;
+    lag_items = most < p.prob[1].items ? most : p.prob[1].items;
+  }
+  // The next item: its product and its index there.
+  __device__ bool next(const GgParams& p, int& which, int& index) {
+    if (phase == 0) {
+      if (i < p.prob[0].items) {
+        which = 0;
+        index = i;
+        i += pairs;
+        return true;
+      }
+      phase = lag_pairs > 0 && lag >= 0 ? 1 : 2;
+      i = phase == 1 ? lag : lag_items + pair;
+    }
+    if (phase == 1) {
+      if (i < lag_items) {
+        which = 1;
+        index = i;
+        i += lag_pairs;
+        return true;
+      }
+      phase = 2;
+      i = lag_items + pair;
+    }
+    if (i < p.prob[1].items) {
+      which = 1;
+      index = i;
+      i += pairs;
+      return true;
+    }
+    return false;
+  }
+};
+
+// Item of a product -> (row tile, column tile, split).  Items run in bands of
+// `band` row tiles, the split outermost and the row tile fastest, so that the
+// items in flight at a time form a block of D about as tall as wide and share
+// the operand stages they read through L2.
+__device__ __forceinline__ void gg_item(const GgProblem& p, int i, int& mt, int& nt, int& sp) {
   const int tiles = p.m_tiles * p.n_tiles;
   sp = i / tiles;
   const int t = i - sp * tiles;
@@ -127,14 +191,13 @@ __device__ __forceinline__ void gg_item(const GgParams& p, int i, int& mt, int& 
   mt = m0 + (r - nt * bsize);
 }
 
-__device__ __forceinline__ int gg_first_stage(const GgParams& p, int sp) {
+__device__ __forceinline__ int gg_first_stage(const GgProblem& p, int sp) {
   return static_cast<int>(static_cast<long long>(p.stages_total) * sp / p.splits);
 }
 
-template <int BN, bool A_MN>
+template <int BN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
-    grad_gemm_kernel(const __grid_constant__ CUtensorMap tm_a,
-                     const __grid_constant__ CUtensorMap tm_b, const GgParams p) {
+    grad_gemm_kernel(const __grid_constant__ GgMaps maps, const __grid_constant__ GgParams p) {
   using Cfg = GgCfg<BN>;
   constexpr int S = Cfg::kStages;
   constexpr int SB = Cfg::kStageBytes;
@@ -170,8 +233,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
     fence_barrier_init();
   }
   if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tm_a);
-    tma_prefetch_desc(&tm_b);
+    for (int w = 0; w < 2; ++w) {
+      if (p.prob[w].items == 0) continue;
+      tma_prefetch_desc(&maps.a[w]);
+      tma_prefetch_desc(&maps.b[w]);
+    }
   }
   if (warp == kGgMmaWarp) {
     tmem_alloc_pair(smem_u32(tmem_slot), 2 * BN);
@@ -191,11 +257,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
       const uint64_t pol = l2_policy_evict_normal();
       long long i = 0;
       bool ok = true;
-      for (int it = pair; ok && it < p.items; it += p.pairs) {
+      GgWalk walk(p, pair);
+      int which, index;
+      while (ok && walk.next(p, which, index)) {
+        const GgProblem& pr = p.prob[which];
         int mt, nt, sp;
-        gg_item(p, it, mt, nt, sp);
-        const int s1 = gg_first_stage(p, sp + 1);
-        for (int u = gg_first_stage(p, sp); u < s1; ++u, ++i) {
+        gg_item(pr, index, mt, nt, sp);
+        const int s1 = gg_first_stage(pr, sp + 1);
+        for (int u = gg_first_stage(pr, sp); u < s1; ++u, ++i) {
           if (i % P != warp) continue;
           const int stage = static_cast<int>(i % S);
           if (i >= S &&
@@ -211,16 +280,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
           const int m0 = mt * kGgTileM + static_cast<int>(rank) * 128;
           const int n0 = nt * BN + static_cast<int>(rank) * (BN / 2);
           const int t0 = u * kGgStageK;
-          if (A_MN) {
+          const CUtensorMap* ta = &maps.a[which];
+          const CUtensorMap* tb = &maps.b[which];
+          if (pr.a_mn) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-              tma_load_2d_pair(a_dst + h * kGgStageK * kGgChunk, &tm_a, m0 + 64 * h, t0, full, pol);
+              tma_load_2d_pair(a_dst + h * kGgStageK * kGgChunk, ta, m0 + 64 * h, t0, full, pol);
           } else {
-            tma_load_2d_pair(a_dst, &tm_a, t0, m0, full, pol);
+            tma_load_2d_pair(a_dst, ta, t0, m0, full, pol);
           }
 #pragma unroll
           for (int h = 0; h < BN / 128; ++h)
-            tma_load_2d_pair(b_dst + h * kGgStageK * kGgChunk, &tm_b, n0 + 64 * h, t0, full, pol);
+            tma_load_2d_pair(b_dst + h * kGgStageK * kGgChunk, tb, n0 + 64 * h, t0, full, pol);
         }
       }
       if (!ok && rank == 0) {
@@ -242,10 +313,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
       uint32_t acc_phase = 0;
       bool ok = true;
       bool ready = false;   // the next stage's barrier already seen complete
-      for (int it = pair; ok && it < p.items; it += p.pairs) {
-        int mt, nt, sp;
-        gg_item(p, it, mt, nt, sp);
-        const int count = gg_first_stage(p, sp + 1) - gg_first_stage(p, sp);
+      GgWalk walk(p, pair);
+      int which, index;
+      while (ok && walk.next(p, which, index)) {
+        const GgProblem& pr = p.prob[which];
+        const int sp = index / (pr.m_tiles * pr.n_tiles);
+        const int count = gg_first_stage(pr, sp + 1) - gg_first_stage(pr, sp);
+        const uint32_t idesc = pr.idesc;
+        // K-major: 8-row groups 1024 bytes apart, 16 t = 32 bytes on.
+        // MN-major: 64-wide chunks kGgStageK rows apart (leading offset),
+        // groups of 8 t 1024 bytes apart, 16 t = two groups on.
+        const uint32_t a_lbo = pr.a_mn ? kGgStageK * kGgChunk : 16;
+        const uint32_t a_step = pr.a_mn ? 2048 : 32;
         if (!mbar_wait_cluster_warp(smem_u32(&acce_bar[acc]), acc_phase ^ 1u, abort_flag)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
@@ -261,15 +340,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
           const uint32_t b_addr = a_addr + Cfg::kABytes;
 #pragma unroll
           for (int j = 0; j < kGgStageK / 16; ++j) {
-            // K-major: 8-row groups 1024 bytes apart, 16 t = 32 bytes on.
-            // MN-major: 64-wide chunks kGgStageK rows apart (leading offset),
-            // groups of 8 t 1024 bytes apart, 16 t = two groups on.
-            const uint64_t adesc =
-                A_MN ? smem_desc(a_addr + j * 2048, kGgStageK * kGgChunk, 1024, kSwizzle128)
-                     : smem_desc(a_addr + j * 32, 16, 1024, kSwizzle128);
+            const uint64_t adesc = smem_desc(a_addr + j * a_step, a_lbo, 1024, kSwizzle128);
             const uint64_t bdesc =
                 smem_desc(b_addr + j * 2048, kGgStageK * kGgChunk, 1024, kSwizzle128);
-            mma_bf16_pair_w(d_tmem, adesc, bdesc, p.idesc, (u > 0 || j > 0) ? 1u : 0u);
+            mma_bf16_pair_w(d_tmem, adesc, bdesc, idesc, (u > 0 || j > 0) ? 1u : 0u);
             if (j == 0) ready = mbar_test_warp(smem_u32(&full_bar[next_stage]), next_phase);
           }
           tc_commit_pair_mc_w(smem_u32(&empty_bar[stage]), 0x3);
@@ -294,11 +368,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
     for (int b = 0; b < 2; ++b) acce_leader[b] = map_to_cta(smem_u32(&acce_bar[b]), 0);
     int acc = 0;
     uint32_t acc_phase = 0;
-    for (int it = pair; it < p.items; it += p.pairs) {
+    GgWalk walk(p, pair);
+    int which, index;
+    while (walk.next(p, which, index)) {
+      const GgProblem& pr = p.prob[which];
       int mt, nt, sp;
-      gg_item(p, it, mt, nt, sp);
+      gg_item(pr, index, mt, nt, sp);
       const int r = mt * kGgTileM + static_cast<int>(rank) * 128 + q * 32 + lane;
-      const float rs = p.row_scale != nullptr && r < p.rows ? 1.0f / __ldg(p.row_scale + r) : 1.0f;
+      const float rs = pr.row_scale != nullptr && r < pr.rows ? 1.0f / __ldg(pr.row_scale + r) : 1.0f;
       int ok = 1;
       if (lane == 0) ok = mbar_wait(smem_u32(&accf_bar[acc]), acc_phase, abort_flag) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -307,7 +384,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
       const uint32_t t_row =
           tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
       long long out_row = r;
-      if (p.pair_rows != 0) out_row = (r & 1) ? p.pair_rows + (r >> 1) : (r >> 1);
+      if (pr.pair_rows != 0) out_row = (r & 1) ? pr.pair_rows + (r >> 1) : (r >> 1);
 #pragma unroll 1
       for (int c = half; c < BN / 32; c += 2) {
         uint32_t v[2][16];
@@ -318,11 +395,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int col = c0 + 16 * h;
-          if (r >= p.rows || col >= p.cols) continue;
-          if (p.splits > 1) {
-            float* dst = p.partial +
-                         (static_cast<long long>(sp) * p.rows + r) * static_cast<long long>(p.cols) +
-                         col;
+          if (r >= pr.rows || col >= pr.cols) continue;
+          if (pr.splits > 1) {
+            float* dst = pr.partial +
+                         (static_cast<long long>(sp) * pr.rows + r) * pr.cols + col;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               *reinterpret_cast<uint4*>(dst + 4 * j) =
@@ -335,7 +411,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
                   __uint_as_float(v[h][2 * j]) * rs, __uint_as_float(v[h][2 * j + 1]) * rs);
               w[j] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-            __nv_bfloat16* dst = p.d + out_row * p.ld_d + col;
+            __nv_bfloat16* dst = pr.d + out_row * pr.cols + col;
             *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
             *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
           }
@@ -356,205 +432,257 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
   if (warp == kGgMmaWarp) tmem_dealloc_pair(tmem_base, 2 * BN);
 }
 
+// ------------------------------------------------------------------ join
+
+struct JoinParams {
+  GgProblem prob[2];      // those with splits > 1 are joined
+  int blocks[2];          // blocks of each
+  const float* sums;      // [runs][cols] column sums, or null
+  __nv_bfloat16* dbias;
+  int runs, cols;
+  int pair_rows;          // as in GgProblem, for the columns
+};
+
 // D = the sum of the splits' partial sums, in split order, scaled and rounded
-// once.
-// One thread per 8 columns.
-__global__ void __launch_bounds__(256)
-    grad_gemm_join_kernel(const float* __restrict__ partial, int splits, int rows, int cols,
-                          const float* __restrict__ row_scale, __nv_bfloat16* __restrict__ d,
-                          long long ld_d, int pair_rows) {
+// once (one thread per 8 columns); then, in blocks of their own, the bias
+// gradient: 32 columns a block, each of 8 row lanes adding every eighth run,
+// the lanes added in order.
+__global__ void __launch_bounds__(256) backward_join_kernel(const __grid_constant__ JoinParams p) {
   grid_dependents_launch();
   grid_dependency_wait();
-  const long long vecs = static_cast<long long>(rows) * (cols / 8);
-  const long long plane = static_cast<long long>(rows) * cols;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < vecs;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const long long r = i / (cols / 8);
-    const int c = static_cast<int>(i - r * (cols / 8)) * 8;
-    float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const float* src = partial + r * cols + c;
-    for (int sp = 0; sp < splits; ++sp, src += plane) {
-      const float4 a = __ldcs(reinterpret_cast<const float4*>(src));
-      const float4 b = __ldcs(reinterpret_cast<const float4*>(src + 4));
-      s[0] += a.x; s[1] += a.y; s[2] += a.z; s[3] += a.w;
-      s[4] += b.x; s[5] += b.y; s[6] += b.z; s[7] += b.w;
+  int block = blockIdx.x;
+  for (int w = 0; w < 2; ++w) {
+    if (block >= p.blocks[w]) {
+      block -= p.blocks[w];
+      continue;
     }
-    const float rs = row_scale != nullptr ? 1.0f / row_scale[r] : 1.0f;
-    uint32_t w[4];
+    const GgProblem& pr = p.prob[w];
+    const long long plane = static_cast<long long>(pr.rows) * pr.cols;
+    // 16 rows of 16 vectors a block and step
+    for (long long r = static_cast<long long>(block) * 16 + threadIdx.x / 16; r < pr.rows;
+         r += static_cast<long long>(p.blocks[w]) * 16)
+    for (int c = threadIdx.x % 16 * 8; c < pr.cols; c += 128) {
+      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      const float* src = pr.partial + r * pr.cols + c;
+#pragma unroll 4
+      for (int sp = 0; sp < pr.splits; ++sp) {
+        const float4 a = __ldcs(reinterpret_cast<const float4*>(src + sp * plane));
+        const float4 b = __ldcs(reinterpret_cast<const float4*>(src + sp * plane + 4));
+        v[0] += a.x; v[1] += a.y; v[2] += a.z; v[3] += a.w;
+        v[4] += b.x; v[5] += b.y; v[6] += b.z; v[7] += b.w;
+      }
+      const float rs = pr.row_scale != nullptr ? 1.0f / pr.row_scale[r] : 1.0f;
+      uint32_t o[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(s[2 * j] * rs, s[2 * j + 1] * rs);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b2);
+      for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * j] * rs, v[2 * j + 1] * rs);
+        o[j] = *reinterpret_cast<const uint32_t*>(&b2);
+      }
+      long long row = r;
+      if (pr.pair_rows != 0) row = (r & 1) ? pr.pair_rows + (r >> 1) : (r >> 1);
+      *reinterpret_cast<uint4*>(pr.d + row * pr.cols + c) = make_uint4(o[0], o[1], o[2], o[3]);
     }
-    long long row = r;
-    if (pair_rows != 0) row = (r & 1) ? pair_rows + (r >> 1) : (r >> 1);
-    *reinterpret_cast<uint4*>(d + row * ld_d + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    return;
   }
+  __shared__ float lanes[8][32];
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  const long long c = static_cast<long long>(block) * 32 + tx;
+  float s = 0.0f;
+  if (c < p.cols) {
+#pragma unroll 8
+    for (int y = ty; y < p.runs; y += 8) s += p.sums[static_cast<long long>(y) * p.cols + c];
+  }
+  lanes[ty][tx] = s;
+  __syncthreads();
+  if (ty != 0 || c >= p.cols) return;
+  for (int j = 1; j < 8; ++j) s += lanes[j][tx];
+  long long at = c;
+  if (p.pair_rows != 0) at = (c & 1) ? p.pair_rows + (c >> 1) : (c >> 1);
+  p.dbias[at] = __float2bfloat16_rn(s);
 }
 
-// ------------------------------------------------------------------ operands
+// ------------------------------------------------------------------ prologue
+
+// What the gradient products read, made in one launch; each part has blocks of
+// its own (0: not needed).
+struct PrologueParams {
+  int blocks[4];
+  // 0: the expanded weight
+  const uint8_t* packed;
+  const float* s_w;             // or null
+  int w_fmt;
+  long long rows, k;
+  __nv_bfloat16* what;
+  // 1: the expanded checkpoint
+  const uint8_t* a_q;
+  const float* s_a;             // or null
+  int a_fmt;
+  long long m;
+  __nv_bfloat16* xhat;
+  // 2: dy [m][ld_dy] copied to rows of ld_copy
+  const __nv_bfloat16* dy;
+  long long ld_dy;
+  __nv_bfloat16* copy;
+  long long ld_copy;
+  // 3: column sums of dy over runs of rows
+  float* sums;                  // [runs][rows]
+  int runs, sums_by_16;         // sums_by_16: dy's rows may be read 16 bytes at a time
+};
 
 // Two FP8 codes -> two floats (exact), first from the low byte.
-template <int kFmt>
-__device__ __forceinline__ float2 fp8_pair_to_float(uint32_t codes) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(codes),
-                                                   Fp8Out<kFmt>::kInterp);
+__device__ __forceinline__ float2 fp8_pair_to_float(uint32_t codes, int fmt) {
+  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+      static_cast<__nv_fp8x2_storage_t>(codes), fmt == SFP8_E5M2 ? __NV_E5M2 : __NV_E4M3);
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// The expanded weight What[r, k] = bf16(dec(W_q[r, k]) * s_w[r]), dense: one
-// thread per 32 k of a row (16 kept codes, 8 index nibbles), reading the
-// packed tile and writing 64 contiguous bytes.  With s_w the one rounding
-// (half a bf16 step) is that of the operand; without it (null: the scales are
-// in dz) the codes are exact in bf16.  What has the weight's true rows only
-// (padding rows are not written).
-template <int kFmt>
-__global__ void __launch_bounds__(256)
-    expand_weight_kernel(const uint8_t* __restrict__ packed, const float* __restrict__ s_w,
-                         long long rows, long long k, __nv_bfloat16* __restrict__ out) {
-  grid_dependents_launch();
-  grid_dependency_wait();
-  const long long chunks = k / 32;
-  const long long ktiles = k / 128;
-  const long long total = rows * chunks;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const long long row = i / chunks;
-    const long long c = i - row * chunks;
-    const int r = static_cast<int>(row % 128);
-    const int j = static_cast<int>(c % 4);
-    const uint8_t* tile = packed + ((row / 128) * ktiles + c / 4) * 10240;
-    const uint4 v = __ldg(
-        reinterpret_cast<const uint4*>(tile + 64 * r + (16 * j ^ (16 * (r >> 1 & 3)))));
-    const uint32_t meta = __ldg(reinterpret_cast<const uint32_t*>(tile + 8192 + 16 * r + 4 * j));
-    const float s = s_w != nullptr ? __ldg(s_w + row) : 1.0f;
-    const uint32_t vals[4] = {v.x, v.y, v.z, v.w};
-    uint32_t w[16];
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  const __nv_bfloat162 b2 = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b2);
+}
+
+// What[r, k] = bf16(dec(W_q[r, k]) * s_w[r]), dense, a 128 x 128 tile of the
+// packed weight at a time: every thread takes 8 pieces of 8 k (4 kept codes, 2
+// index nibbles), neighbouring threads neighbouring words of the tile and
+// neighbouring 16-byte vectors of a row.  With s_w the one rounding (half a
+// bf16 step) is that of the operand; without it (null: the scales are in dz)
+// the codes are exact in bf16.
+__device__ __forceinline__ void expand_weight(const PrologueParams& p, int block) {
+  const int ktiles = static_cast<int>(p.k / 128);
+  const long long tiles = (p.rows + 127) / 128 * ktiles;
+  for (long long t = block; t < tiles; t += p.blocks[0]) {
+    const long long nt = t / ktiles;
+    const uint8_t* tile = p.packed + t * 10240;
+    const long long row0 = nt * 128;
+    __nv_bfloat16* out = p.what + row0 * p.k + (t - nt * ktiles) * 128;
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      const float2 f = fp8_pair_to_float<kFmt>((vals[g / 2] >> (16 * (g % 2))) & 0xFFFFu);
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * s, f.y * s);
-      const uint32_t bits = *reinterpret_cast<const uint32_t*>(&b2);
-      const uint32_t nib = (meta >> (4 * g)) & 0xFu;
-      // the group's four bf16 as one 64-bit word
-      const unsigned long long word =
-          (static_cast<unsigned long long>(bits & 0xFFFFu) << (16 * (nib & 3u))) |
-          (static_cast<unsigned long long>(bits >> 16) << (16 * (nib >> 2)));
-      w[2 * g] = static_cast<uint32_t>(word);
-      w[2 * g + 1] = static_cast<uint32_t>(word >> 32);
+    for (int i = 0; i < 8; ++i) {
+      const int item = i * 256 + threadIdx.x;
+      const int r = item / 16, j = item % 16;
+      if (row0 + r >= p.rows) continue;
+      const uint32_t vals = __ldg(reinterpret_cast<const uint32_t*>(
+          tile + 64 * r + (((j / 4) ^ (r >> 1 & 3)) * 16) + (j % 4) * 4));
+      const uint32_t meta = __ldg(tile + 8192 + 16 * r + j);
+      const float s = p.s_w != nullptr ? __ldg(p.s_w + row0 + r) : 1.0f;
+      uint32_t w[4];
+#pragma unroll
+      for (int g = 0; g < 2; ++g) {
+        const float2 f = fp8_pair_to_float((vals >> (16 * g)) & 0xFFFFu, p.w_fmt);
+        const uint32_t bits = bf16_pair(f.x * s, f.y * s);
+        const uint32_t nib = (meta >> (4 * g)) & 0xFu;
+        // the group's four bf16 as one 64-bit word
+        const unsigned long long word =
+            (static_cast<unsigned long long>(bits & 0xFFFFu) << (16 * (nib & 3u))) |
+            (static_cast<unsigned long long>(bits >> 16) << (16 * (nib >> 2)));
+        w[2 * g] = static_cast<uint32_t>(word);
+        w[2 * g + 1] = static_cast<uint32_t>(word >> 32);
+      }
+      *reinterpret_cast<uint4*>(out + r * p.k + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    uint4* dst = reinterpret_cast<uint4*>(out + row * k + c * 32);
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-      dst[t] = make_uint4(w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]);
   }
 }
 
-// The expanded checkpoint xhat[m, k] = bf16(dec(A_q[m, k]) * s_a[m]), or with
-// s null the codes' own values: one thread per 16 codes.
-template <int kFmt>
-__global__ void __launch_bounds__(256)
-    expand_rows_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s, long long rows,
-                       long long cols, __nv_bfloat16* __restrict__ out) {
-  grid_dependents_launch();
-  grid_dependency_wait();
-  const long long per_row = cols / 16;
-  const long long total = rows * per_row;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(q) + i);
-    const float sc = s != nullptr ? __ldg(s + i / per_row) : 1.0f;
-    const uint32_t in[4] = {v.x, v.y, v.z, v.w};
-    uint32_t w[8];
+// xhat[m, k] = bf16(dec(A_q[m, k]) * s_a[m]), or with s_a null the codes' own
+// values, 128 x 128 at a time as above.
+__device__ __forceinline__ void expand_rows(const PrologueParams& p, int block) {
+  const int ktiles = static_cast<int>(p.k / 128);
+  const long long tiles = (p.m + 127) / 128 * ktiles;
+  for (long long t = block; t < tiles; t += p.blocks[1]) {
+    const long long mt = t / ktiles;
+    const long long row0 = mt * 128;
+    const long long at = row0 * p.k + (t - mt * ktiles) * 128;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 f = fp8_pair_to_float<kFmt>((in[j / 2] >> (16 * (j % 2))) & 0xFFFFu);
-      const __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-      w[j] = *reinterpret_cast<const uint32_t*>(&b2);
+    for (int i = 0; i < 8; ++i) {
+      const int item = i * 256 + threadIdx.x;
+      const int r = item / 16, j = item % 16;
+      if (row0 + r >= p.m) continue;
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.a_q + at + r * p.k + 8 * j));
+      const float s = p.s_a != nullptr ? __ldg(p.s_a + row0 + r) : 1.0f;
+      uint32_t w[4];
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const float2 f =
+            fp8_pair_to_float(((h < 2 ? v.x : v.y) >> (16 * (h % 2))) & 0xFFFFu, p.a_fmt);
+        w[h] = bf16_pair(f.x * s, f.y * s);
+      }
+      *reinterpret_cast<uint4*>(p.xhat + at + r * p.k + 8 * j) =
+          make_uint4(w[0], w[1], w[2], w[3]);
     }
-    uint4* dst = reinterpret_cast<uint4*>(out) + 2 * i;
-    dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
 }
 
-// dy [m][ld] -> out [m][ld_out] (ld_out >= cols, columns past cols zero), for
-// a dy whose base or row stride TMA cannot take.  One thread per element.
-__global__ void __launch_bounds__(256)
-    copy_rows_kernel(const __nv_bfloat16* __restrict__ in, long long rows, long long cols,
-                     long long ld, __nv_bfloat16* __restrict__ out, long long ld_out) {
-  grid_dependents_launch();
-  grid_dependency_wait();
-  const long long total = rows * ld_out;
-  for (long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<long long>(gridDim.x) * blockDim.x) {
-    const long long r = i / ld_out;
-    const long long c = i - r * ld_out;
-    out[i] = c < cols ? in[r * ld + c] : __float2bfloat16_rn(0.0f);
+// dy to rows of ld_copy elements (a multiple of 8), for a dy whose base or
+// row stride TMA cannot take; zeros past its columns.  A row per block and
+// step, 8 elements a thread.
+__device__ __forceinline__ void copy_dy(const PrologueParams& p, int block) {
+  for (long long r = block; r < p.m; r += p.blocks[2]) {
+    const unsigned short* src = reinterpret_cast<const unsigned short*>(p.dy) + r * p.ld_dy;
+    for (long long c = threadIdx.x * 8; c < p.ld_copy; c += 256 * 8) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = c + j < p.rows ? __ldg(src + c + j) : 0u;
+      *reinterpret_cast<uint4*>(p.copy + r * p.ld_copy + c) =
+          make_uint4(v[0] | (v[1] << 16), v[2] | (v[3] << 16), v[4] | (v[5] << 16),
+                     v[6] | (v[7] << 16));
+    }
   }
 }
 
-// Column sums of dz [rows][ld] for the bias gradient, in fp32, in two steps:
-// block (x, y) adds the rows of its run y for 64 columns (8 row lanes x 32
-// column pairs) into partial[y][cols]; the second kernel adds the runs in
-// order and rounds once.  row_scale and col_scale, where given, are divided
-// out (a gated block's dz holds both).
-constexpr int kColSumCols = 64;
-__global__ void __launch_bounds__(256)
-    column_sums_kernel(const __nv_bfloat16* __restrict__ dz, long long rows, long long cols,
-                       long long ld, const float* __restrict__ row_scale,
-                       float* __restrict__ partial) {
-  grid_dependents_launch();
-  grid_dependency_wait();
-  __shared__ float2 sums[8][32];
-  const int x = threadIdx.x % 32, y = threadIdx.x / 32;
-  const long long col = static_cast<long long>(blockIdx.x) * kColSumCols + 2 * x;
-  const long long r0 = rows * blockIdx.y / gridDim.y, r1 = rows * (blockIdx.y + 1) / gridDim.y;
-  float2 s = make_float2(0.0f, 0.0f);
-  if (col + 1 < cols && ld % 2 == 0 && (reinterpret_cast<uintptr_t>(dz) & 3u) == 0) {
+// Column sums of dy, in fp32: block (x, y) adds the rows of its run y for 256
+// columns, 8 row lanes of 32 threads with 8 columns each.
+constexpr int kColSumCols = 256;
+__device__ __forceinline__ void sum_columns(const PrologueParams& p, int block,
+                                            float (&lanes)[8][kColSumCols]) {
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  const long long c0 = static_cast<long long>(block / p.runs) * kColSumCols;
+  const int run = block % p.runs;
+  const long long r0 = p.m * run / p.runs, r1 = p.m * (run + 1) / p.runs;
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  // 16-byte reads: 8 neighbouring columns; else every 32nd
+  const bool vec = p.sums_by_16 && c0 + 8 * tx + 8 <= p.rows;
+  if (vec) {
+    const __nv_bfloat16* src = p.dy + c0 + 8 * tx;
 #pragma unroll 4
-    for (long long r = r0 + y; r < r1; r += 8) {
-      const float2 v =
-          __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(dz + r * ld + col));
-      const float rs = row_scale != nullptr ? 1.0f / row_scale[r] : 1.0f;
-      s.x = fmaf(v.x, rs, s.x);
-      s.y = fmaf(v.y, rs, s.y);
+    for (long long r = r0 + ty; r < r1; r += 8) {
+      float f[8];
+      InputTraits<__nv_bfloat16>::to_float(
+          __ldg(reinterpret_cast<const uint4*>(src + r * p.ld_dy)), f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[j] += f[j];
     }
-  } else if (col < cols) {
-    for (long long r = r0 + y; r < r1; r += 8) {
-      const float rs = row_scale != nullptr ? 1.0f / row_scale[r] : 1.0f;
-      s.x = fmaf(__bfloat162float(dz[r * ld + col]), rs, s.x);
-      if (col + 1 < cols) s.y = fmaf(__bfloat162float(dz[r * ld + col + 1]), rs, s.y);
+  } else {
+    const int step = p.sums_by_16 ? 1 : 32;
+    const long long first = c0 + (p.sums_by_16 ? 8 * tx : tx);
+    for (long long r = r0 + ty; r < r1; r += 8) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (first + j * step < p.rows) s[j] += __bfloat162float(p.dy[r * p.ld_dy + first + j * step]);
     }
   }
-  sums[y][x] = s;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) lanes[ty][p.sums_by_16 ? 8 * tx + j : tx + 32 * j] = s[j];
   __syncthreads();
-  if (y == 0 && col < cols) {
-    for (int j = 1; j < 8; ++j) {
-      s.x += sums[j][x].x;
-      s.y += sums[j][x].y;
-    }
-    float* dst = partial + static_cast<long long>(blockIdx.y) * cols + col;
-    dst[0] = s.x;
-    if (col + 1 < cols) dst[1] = s.y;
+  const long long c = c0 + threadIdx.x;
+  if (c < p.rows) {
+    float t = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t += lanes[j][threadIdx.x];
+    p.sums[run * p.rows + c] = t;
   }
 }
 
-// out[c] = the runs' sums added in order; with pair_rows, column c goes to
-// (c & 1) * pair_rows + c / 2 (a gated block's gate and up values).
 __global__ void __launch_bounds__(256)
-    column_sums_join_kernel(const float* __restrict__ partial, int runs, long long cols,
-                            const float* __restrict__ col_scale, __nv_bfloat16* __restrict__ out, long long pair_rows) {
+    backward_prologue_kernel(const __grid_constant__ PrologueParams p) {
+  __shared__ float lanes[8][kColSumCols];
   grid_dependents_launch();
   grid_dependency_wait();
-  const long long c = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  if (c >= cols) return;
-  float s = 0.0f;
-  for (int y = 0; y < runs; ++y) s += partial[y * cols + c];
-  if (col_scale != nullptr) s /= col_scale[c];
-  long long at = c;
-  if (pair_rows != 0) at = (c & 1) ? pair_rows + (c >> 1) : (c >> 1);
-  out[at] = __float2bfloat16_rn(s);
+  int block = blockIdx.x;
+  int part = 0;
+  while (block >= p.blocks[part]) block -= p.blocks[part++];
+  if (part == 0) expand_weight(p, block);
+  else if (part == 1) expand_rows(p, block);
+  else if (part == 2) copy_dy(p, block);
+  else sum_columns(p, block, lanes);
 }
 
 }  // namespace sfp8

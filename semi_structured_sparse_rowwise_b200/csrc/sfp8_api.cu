@@ -586,6 +586,7 @@ struct GatedCall {
   const void* dh;   // kEpiGatedGrad: [m, hidden] bf16, row stride ld_dh
   int64_t ld_dh;
   int64_t ld_out;   // row stride of the output
+  float* col_sums;  // kEpiGatedGrad: [m_tiles * parts][n] sums over tokens, or null
 };
 
 template <int BN, int KS, bool RA, bool FQ = false, int EPI = kEpiLinear>
@@ -769,7 +770,7 @@ sfp8_status launch_pair_cfg(DeviceInfo* dev, const LinearPlan& pl, const void* a
                             sfp8_dtype a_dtype, const float* s_a, int64_t m, const void* packed,
                             sfp8_dtype w_dtype, const float* s_w, int64_t n, int64_t k,
                             const void* bias, void* y, cudaStream_t st, const GatedCall* gc) {
-  using Cfg = PairCfg<KS, WT>;
+  using Cfg = PairCfg<KS, WT, EPI>;
   auto kern = sparse_linear_pair_kernel<KS, WT, EPI>;
   constexpr int slot = EPI * 4 + (KS - 1) * 2 + (WT - 1);
   {
@@ -840,6 +841,7 @@ sfp8_status launch_pair_cfg(DeviceInfo* dev, const LinearPlan& pl, const void* a
     prm.dh = static_cast<const __nv_bfloat16*>(gc->dh);
     prm.ld_dh = gc->ld_dh;
     prm.ld_out = gc->ld_out;
+    prm.col_sums = gc->col_sums;
   }
   return launch_dependent(kern, dim3(2 * pairs), dim3(Cfg::kThreads), pl.smem_bytes, st, tw2,
                           tw, ta, prm);
@@ -1732,7 +1734,7 @@ sfp8_status sfp8_gated_linear(const void* a_q, sfp8_dtype a_dtype, const float* 
   unsigned int* counters = need > 0 ? reinterpret_cast<unsigned int*>(
                                           static_cast<uint8_t*>(workspace) + pl.partial_bytes)
                                     : nullptr;
-  const GatedCall gc{kEpiGated, act, nullptr, 0, n};
+  const GatedCall gc{kEpiGated, act, nullptr, 0, n, nullptr};
   return launch_linear(dev, pl, a_q, a_dtype, s_a, m, packed, w_dtype, s_w, 2 * n, k, bias, h,
                        static_cast<float*>(workspace), counters,
                        static_cast<cudaStream_t>(stream), nullptr, 0, nullptr, &gc);
@@ -1750,7 +1752,7 @@ sfp8_status sfp8_gated_linear_quant(const void* x, sfp8_dtype x_dtype, int64_t l
                                     void* stream) {
   const sfp8_status s = validate_gated(n, act);
   if (s != SFP8_OK) return s;
-  const GatedCall gc{kEpiGated, act, nullptr, 0, n};
+  const GatedCall gc{kEpiGated, act, nullptr, 0, n, nullptr};
   return quant_linear(x, x_dtype, ld_x, a_dtype, a_q, s_a, m, packed, w_dtype, s_w, 2 * n, k,
                       bias, h, workspace, workspace_bytes, stream, kQuantChained, &gc);
 }

@@ -32,10 +32,10 @@
 //               commits multicast to both CTAs' barriers), the whole warp
 //               walking the loop and one elected lane issuing.  Rank 1: only
 //               allocates and frees tensor memory with rank 0.
-//   warps 5-    epilogue: two warps per tensor-memory lane quadrant (and
-//               weight slot), each taking every other 16-column chunk of the
-//               accumulator: tensor memory -> registers -> scale/bias/bf16
-//               -> global.
+//   warps 5-    epilogue: two warps (or four, PairCfg::kEpiParts) per
+//               tensor-memory lane quadrant and weight slot, each taking
+//               every other (fourth) 16-column chunk of the accumulator:
+//               tensor memory -> registers -> scale/bias/bf16 -> global.
 // Work split: tile t -> (weight group, token tile) in bands of token tiles
 // (pair_tile_coords), pair p takes tiles p, p + pairs, ...  No split-K.  Tensor memory: accumulator b at columns
 // [224 b, 224 b + BN), metadata of the stage's k steps at 448.
@@ -69,13 +69,18 @@ constexpr int kPairMetaCol = 2 * kPairMaxTokens;  // after the two accumulators
 //   WT = 1: pair tile 256 x BN, two accumulators (double buffer).
 //   WT = 2: pair tile 512 x BN, one accumulator per weight slot (single
 //           buffer): each activation byte loaded feeds twice the MMAs.
-template <int KS, int WT>
+// The gated epilogues evaluate an activation per pair of accumulator rows, so
+// they get 16 warps however many weight slots there are (with 8, the gradient
+// epilogue took 1071 us of a tile loop whose MMAs take about 500: m = 8192,
+// k = 4096, 2n = 28672).
+template <int KS, int WT, int EPI = kEpiLinear>
 struct PairCfg {
   static_assert(KS == 1 || KS == 2, "1 or 2 k steps per stage");
   static_assert(WT == 1 || WT == 2, "1 or 2 weight tiles per CTA");
   static constexpr int kWBytes = KS * WT * kWTileBytes;
   static constexpr int kMaxStages = 16;
-  static constexpr int kEpiWarps = 8 * WT;       // two per lane quadrant and slot
+  static constexpr int kEpiWarps = EPI == kEpiLinear ? 8 * WT : 16;
+  static constexpr int kEpiParts = kEpiWarps / (4 * WT);   // warps per lane quadrant and slot
   static constexpr int kThreads = 32 * (kPairLoadWarps + 1 + kEpiWarps);
   static_assert(kPairMetaCol + 4 * KS * WT <= kPairTmemCols, "metadata columns must fit");
   // Shared memory of one stage for BN tokens per tile (a multiple of 1024).
@@ -112,6 +117,7 @@ struct PairParams {
   const __nv_bfloat16* dh;  // [m][ld_dh], n / 2 columns (kEpiGatedGrad)
   long long ld_dh;
   long long ld_out;         // row stride of y: h's n / 2, dz's padded width
+  float* col_sums;          // [m_tiles * parts][n] sums of dz over tokens, or null
 };
 
 // Tile t -> (weight group g, token tile mt).  Tiles run in bands of p.band
@@ -137,11 +143,11 @@ __device__ __forceinline__ void load_sa_pair(const PairParams& p, int m0, float 
 }
 
 template <int KS, int WT, int EPI = kEpiLinear>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT, EPI>::kThreads, 1)
     sparse_linear_pair_kernel(const __grid_constant__ CUtensorMap tm_w2,
                               const __grid_constant__ CUtensorMap tm_w,
                               const __grid_constant__ CUtensorMap tm_a, const PairParams p) {
-  using Cfg = PairCfg<KS, WT>;
+  using Cfg = PairCfg<KS, WT, EPI>;
   const int S = p.stages;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -352,10 +358,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
   } else {
     // ------------------------------------------------------------ epilogue
     grid_dependency_wait();
-    const int e = warp - kPairEpiWarp0;      // 0 .. 8 WT - 1
+    constexpr int kParts = Cfg::kEpiParts;
+    const int e = warp - kPairEpiWarp0;      // 0 .. kEpiWarps - 1
     const int q = warp % 4;                   // tensor-memory lane quadrant
-    const int half = (e / 4) % 2;             // 16-column chunks half, half + 2, ...
-    const int slot = e / 8;                   // weight slot (WT = 2)
+    const int part = (e / 4) % kParts;        // 16-column chunks part, part + kParts, ...
+    const int slot = e / (4 * kParts);        // weight slot (WT = 2)
     uint32_t acce_leader[2];
     for (int b = 0; b < 2; ++b) acce_leader[b] = map_to_cta(smem_u32(&acce_bar[b]), 0);
     int acc = 0;
@@ -368,11 +375,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
       const float sw = (n < p.n) ? __ldg(p.s_w + n) : 0.0f;
       const long long bias_at = EPI != kEpiLinear ? gated_bias_index(n, p.n) : n;
       const float bv = (p.bias != nullptr && n < p.n) ? __bfloat162float(p.bias[bias_at]) : 0.0f;
-      float sw_gate = 0.0f, sw_up = 0.0f;
+      const int m_tile0 = mt * p.bn;
+      const int chunks = p.bn / 16;
+      // Gradient: this lane's eight dh of a chunk, loaded one chunk ahead
+      // (the first before the accumulator is waited for).  Addresses past
+      // the end are clamped into the tensor; what they give is not used.
+      float sw_gate = 0.0f, sw_up = 0.0f, sum_gate = 0.0f, sum_up = 0.0f;
+      const int odd8 = (n & 1) * 8;
+      const unsigned short* dh_col = nullptr;
+      unsigned short dh_next[8];
+      auto load_dh = [&](int c) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int m = m_tile0 + c * 16 + odd8 + j;
+          dh_next[j] = __ldg(dh_col + static_cast<long long>(m < p.m ? m : p.m - 1) * p.ld_dh);
+        }
+      };
       if constexpr (EPI == kEpiGatedGrad) {
         const float other = __shfl_xor_sync(0xffffffffu, sw, 1);
         sw_gate = (n & 1) ? other : sw;
         sw_up = (n & 1) ? sw : other;
+        dh_col = reinterpret_cast<const unsigned short*>(p.dh) + ((n < p.n ? n : p.n - 1) >> 1);
+        if (part < chunks) load_dh(part);
       }
       int ok = 1;
       if (lane == 0) ok = mbar_wait(smem_u32(&accf_bar[acc]), acc_phase, abort_flag) ? 1 : 0;
@@ -381,9 +405,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
       tc_fence_after();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                              static_cast<uint32_t>((WT == 1 ? acc : slot) * kPairMaxTokens);
-      const int m_tile0 = mt * p.bn;
 #pragma unroll 1
-      for (int c = half; c < p.bn / 16; c += 2) {
+      for (int c = part; c < chunks; c += kParts) {
         uint32_t r[16];
         tmem_ld_32x32b_x16(t_row + c * 16, r);
         float sa[16];
@@ -400,15 +423,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
             }
           }
         } else {
-          const int first = m_tile0 + c * 16 + (n & 1) * 8;   // this lane's eight tokens
+          const int first = m_tile0 + c * 16 + odd8;   // this lane's eight tokens
           float dh[8];
           if constexpr (EPI == kEpiGatedGrad) {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
-              dh[j] = (n < p.n && first + j < p.m)
-                          ? __bfloat162float(
-                                p.dh[static_cast<long long>(first + j) * p.ld_dh + (n >> 1)])
-                          : 0.0f;
+              dh[j] = __uint_as_float(static_cast<uint32_t>(dh_next[j]) << 16);
+            if (c + kParts < chunks) load_dh(c + kParts);
           }
           tmem_ld_wait();
           float z[16], g[8], u[8];
@@ -426,9 +447,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
                 float f, df;
                 act_value_grad(g[j], p.act, f, df);
                 // gate's and up's gradient with the scales in, neighbours in dz
-                const float d = dh[j] * ((n & 1) ? sa[j + 8] : sa[j]);
+                const float d_gate = dh[j] * u[j] * df, d_up = dh[j] * f;
+                sum_gate += d_gate;
+                sum_up += d_up;
+                const float s = (n & 1) ? sa[j + 8] : sa[j];
                 *reinterpret_cast<__nv_bfloat162*>(row + (n & ~1)) =
-                    __floats2bfloat162_rn(d * u[j] * df * sw_gate, d * f * sw_up);
+                    __floats2bfloat162_rn(d_gate * (s * sw_gate), d_up * (s * sw_up));
               }
             }
           }
@@ -437,6 +461,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT>::kTh
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(acce_leader[acc]);
+      if constexpr (EPI == kEpiGatedGrad) {
+        // the bias gradient's share of these tokens: gate's sum to the gate
+        // lane, up's to the up lane
+        if (p.col_sums != nullptr) {
+          const float mine = (n & 1) ? sum_up : sum_gate;
+          const float theirs =
+              __shfl_xor_sync(0xffffffffu, (n & 1) ? sum_gate : sum_up, 1);
+          if (n < p.n)
+            p.col_sums[static_cast<long long>(mt * kParts + part) * p.n + n] = mine + theirs;
+        }
+      }
       if (WT == 1) {
         acc ^= 1;
         if (acc == 0) acc_phase ^= 1u;
