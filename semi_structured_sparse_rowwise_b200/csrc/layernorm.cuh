@@ -5,27 +5,41 @@
 //   forward   mean = sum_c x / C,   var = sum_c (x - mean)^2 / C
 //             rstd = 1 / sqrt(var + eps)
 //             y    = (x - mean) * rstd * weight + bias
-//             s    = max(max_c |y|, 1e-12) / FP8_MAX,  q = fp8(y / s)
+//             s    = max(max_c |y|, 1e-12) / FP8_MAX,  q = fp8(y * (1 / s))
 //   backward  xh = (x - mean) * rstd,  g = weight * dy
 //             dx = rstd * (g - sum_c g / C - xh * sum_c (g xh) / C)
 //             dweight = sum_rows dy * xh,   dbias = sum_rows dy
 //
 // All of it in fp32; y and dx are rounded once to x's type, the codes once
-// from the fp32 y.  The variance is taken about the mean (two reductions over
+// from the fp32 y (multiplied by the rounded reciprocal of s, where the
+// quantiser of a given tensor divides: the fp32 y is itself a few roundings
+// off, so the quotient's last bit decides nothing).  The variance is taken about the mean (two reductions over
 // values held in registers), never as a difference of two sums.
 //
-// Both passes are bound by memory: a row is read once into the registers of
-// TPR threads (N vectors of VEC elements each), reduced by warp shuffles and,
-// for more than one warp, shared memory, and written from the registers.
+// Both passes are bound by memory.  Kernels by row length and count:
+//   row kernel     few rows (or short ones): one row per group of TPR threads,
+//                  N vectors of VEC elements each in registers, reduced by
+//                  warp shuffles and, for more than one warp, shared memory.
+//   stream kernel  many rows of 1 to 16 KB: one persistent block a SM with
+//                  two to eight row groups of 128 or 256 threads.  Each group
+//                  has a ring of row buffers in shared memory that bulk
+//                  copies keep filled ahead, so that HBM streams through the
+//                  reductions' barriers; the parameters lie in shared memory
+//                  as fp32.  What is left to be short of is instructions and
+//                  the latency of the reductions (a row per 256 threads in
+//                  scalar arithmetic issued 28 million warp instructions for
+//                  8192 rows of 4096 bf16 and took 47 us to codes): hence
+//                  packed fp32 pairs, few and wide threads a row, and in the
+//                  forward pass two rows a group at a time.  8192 x 4096
+//                  bf16: 32 us to codes (3.2 TB/s), 28 us to bf16 (4.7 TB/s),
+//                  46 us backward (4.4 TB/s).
+//   long kernels   rows that fit neither read them again from L2.
 // VEC elements make 16 bytes where base, row stride and width allow, else 1.
-// Rows that do not fit the registers take the loop kernels, which read them
-// again from L2.
 //
-// The backward kernel is persistent: a group of TPR threads walks rows, keeps
-// its columns' dweight and dbias sums in registers, loads the next row before
-// it finishes this one, and writes one partial sum per group at the end; a
-// second kernel adds the groups in order (no atomics: the same bits every
-// time).
+// The backward kernels are persistent too: a group of threads walks rows,
+// keeps its columns' dweight and dbias sums in registers and writes one
+// partial sum per group at the end; a second kernel adds the groups in order
+// (no atomics: the same bits every time).
 #pragma once
 
 #include <type_traits>
@@ -132,13 +146,19 @@ __device__ __forceinline__ void norm_params(const void* p, int f32, int c, float
   }
 }
 
-// Codes of VEC values (VEC 4 or 8) at q.
+// Codes of VEC values (VEC 4 or 8) times r at q.
 template <int VEC>
-__device__ __forceinline__ void norm_codes(uint8_t* q, const float (&f)[VEC], float s, float r,
-                                           int fmt) {
+__device__ __forceinline__ void norm_codes(uint8_t* q, const float (&f)[VEC], float r, int fmt) {
   uint32_t w[VEC / 4];
-  if (fmt == SFP8_E5M2) quantize_vec<SFP8_E5M2, VEC>(f, s, r, w);
-  else quantize_vec<SFP8_E4M3, VEC>(f, s, r, w);
+#pragma unroll
+  for (int i = 0; i < VEC / 4; ++i) {
+    const float* v = &f[4 * i];
+    w[i] = fmt == SFP8_E5M2
+               ? cvt_pair<SFP8_E5M2>(v[0] * r, v[1] * r) |
+                     (cvt_pair<SFP8_E5M2>(v[2] * r, v[3] * r) << 16)
+               : cvt_pair<SFP8_E4M3>(v[0] * r, v[1] * r) |
+                     (cvt_pair<SFP8_E4M3>(v[2] * r, v[3] * r) << 16);
+  }
   store_codes<VEC>(q, w);
 }
 
@@ -244,7 +264,7 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * TPR + t) * VEC;
-      if (c < p.cols) norm_codes<VEC>(qr + c, v[i], s, r, p.q_fmt);
+      if (c < p.cols) norm_codes<VEC>(qr + c, v[i], r, p.q_fmt);
     }
   }
 }
@@ -308,9 +328,303 @@ __global__ void __launch_bounds__(1024)
     if (threadIdx.x == 0) p.scales[row] = s;
     for (long long c = c0; c < cols; c += 1024 * VEC) {
       values(c);
-      norm_codes<VEC>(p.q + row * cols + c, f, s, r, p.q_fmt);
+      norm_codes<VEC>(p.q + row * cols + c, f, r, p.q_fmt);
     }
   }
+}
+
+// ------------------------------------------------------------------ row ring
+
+constexpr int kNormMaxSlots = 8;
+
+
+
+// Ring of row buffers of a row group: slot i % slots holds the group's i-th
+// row (`parts` rows of `bytes` each, from as many tensors).  One thread fills
+// it; the waits are bounded, and after one has run out (the status word says
+// so) the others give up at once and the group runs through on whatever the
+// buffers hold.
+template <int PARTS>
+struct NormRing {
+  uint8_t* base;
+  uint64_t* full;
+  volatile int* abort;
+  uint32_t bytes;     // of one row, a multiple of 16
+  int slots;
+  __device__ uint8_t* slot(int i) const {
+    return base + static_cast<size_t>(i % slots) * PARTS * bytes;
+  }
+  // The group's i-th row, from a (and b).  Every thread must have finished
+  // with the slot's previous row.
+  __device__ void fill(int i, const void* a, const void* b) const {
+    const uint32_t bar = smem_u32(&full[i % slots]);
+    const uint64_t pol = l2_policy_evict_first();
+    uint8_t* dst = slot(i);
+    mbar_arrive_expect_tx(bar, PARTS * bytes);
+    bulk_load(smem_u32(dst), a, bytes, bar, pol);
+    if (PARTS == 2) bulk_load(smem_u32(dst + bytes), b, bytes, bar, pol);
+  }
+  __device__ void wait(int i) const {
+    mbar_wait(smem_u32(&full[i % slots]), static_cast<uint32_t>((i / slots) & 1), abort);
+  }
+  // One thread, after the group's `rows` rows: where waits were given up, lets
+  // the copies still in flight land (again with a limit) before the block
+  // goes on to reuse or leave its shared memory.
+  __device__ void drain(int rows) const {
+    if (!*abort) return;
+    for (int i = rows > slots ? rows - slots : 0; i < rows; ++i) {
+      volatile int no_abort = 0;
+      mbar_wait(smem_u32(&full[i % slots]), static_cast<uint32_t>((i / slots) & 1), &no_abort);
+    }
+  }
+};
+
+// VEC elements at p as pairs of floats.
+template <typename T, int VEC>
+__device__ __forceinline__ void load_pairs(const T* p, float2 (&f)[VEC / 2]) {
+  NormVec<T, VEC> v;
+  v.load(p);
+  float t[VEC];
+  v.floats(t);
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) f[j] = make_float2(t[2 * j], t[2 * j + 1]);
+}
+
+// Parameters in shared memory: fp32, the first four of every vector's VEC in
+// one plane, the other four in the next, so that neighbouring threads read
+// neighbouring 16 bytes.
+template <int VEC>
+__device__ __forceinline__ void shared_pairs(const float* plane, int vec, int cols,
+                                             float2 (&f)[VEC / 2]) {
+#pragma unroll
+  for (int j = 0; j < VEC / 4; ++j) {
+    const float4 t = *reinterpret_cast<const float4*>(plane + j * (cols / (VEC / 4)) + 4 * vec);
+    f[2 * j] = make_float2(t.x, t.y);
+    f[2 * j + 1] = make_float2(t.z, t.w);
+  }
+}
+
+template <typename T, int VEC>
+__device__ __forceinline__ void params_to_shared(const void* p, int f32, float missing, int cols,
+                                                 float* plane) {
+  for (int v = threadIdx.x; v < cols / VEC; v += blockDim.x) {
+    float w[VEC];
+    norm_params<T, VEC>(p, f32, v * VEC, missing, w);
+#pragma unroll
+    for (int j = 0; j < VEC / 4; ++j)
+      *reinterpret_cast<float4*>(plane + j * (cols / (VEC / 4)) + 4 * v) =
+          make_float4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+  }
+}
+
+__device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
+
+// Sums (or maxima of magnitudes) over a row group of TPR threads, ROWS at a
+// time over one barrier of the group's own; `red` holds one value a warp and
+// row and is not written again before the group's next barrier.
+template <int TPR, int ROWS, bool kMax>
+__device__ __forceinline__ void group_reduce(float (&v)[ROWS], float (*red)[TPR / 32], int group) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+      const float t = __shfl_xor_sync(0xffffffffu, v[q], o);
+      v[q] = kMax ? fmaxf(v[q], t) : v[q] + t;
+    }
+  if (threadIdx.x % 32 == 0) {
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) red[q][threadIdx.x % TPR / 32] = v[q];
+  }
+  named_barrier_sync(1 + group, TPR);
+#pragma unroll
+  for (int q = 0; q < ROWS; ++q) {
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < TPR / 128; ++i) {
+      const float4 t = *reinterpret_cast<const float4*>(&red[q][4 * i]);
+      s = kMax ? fmaxf(s, fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)))
+               : s + ((t.x + t.y) + (t.z + t.w));
+    }
+    v[q] = s;
+  }
+}
+
+// Shared memory of a stream kernel: the parameters (`params` vectors of
+// `cols` floats), then the groups' rings.
+__host__ __device__ constexpr int norm_stream_smem(int groups, int params, int cols, int parts,
+                                                   int row_bytes, int slots) {
+  return params * cols * 4 + groups * slots * parts * row_bytes;
+}
+
+// N vectors of VEC elements a thread: cols <= TPR * N * VEC, a multiple of VEC.
+// A group takes ROWS rows at a time: their reductions share the barriers and
+// overlap, and the parameters are read from shared memory once for all.
+template <typename T, int VEC, int TPR, int N, int ROWS, int THREADS, bool Q>
+__global__ void __launch_bounds__(THREADS, 1)
+    layernorm_stream_kernel(const NormParams p, int slots) {
+  extern __shared__ __align__(128) uint8_t norm_smem[];
+  static_assert(THREADS % TPR == 0, "whole row groups");
+  constexpr int kGroups = THREADS / TPR;
+  __shared__ uint64_t full[kGroups][kNormMaxSlots];
+  __shared__ int abort_flag;
+  __shared__ __align__(16) float red[kGroups][3][ROWS][TPR / 32];
+  grid_dependents_launch();
+  const int group = threadIdx.x / TPR;
+  const int t = threadIdx.x % TPR;
+  float* w_sm = reinterpret_cast<float*>(norm_smem);
+  float* b_sm = w_sm + p.cols;
+  const uint32_t bytes = static_cast<uint32_t>(p.cols * sizeof(T));
+  const NormRing<1> ring{norm_smem + 8ll * p.cols + static_cast<size_t>(group) * slots * bytes,
+                         full[group], &abort_flag, bytes, slots};
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < kGroups; ++g)
+      for (int s = 0; s < slots; ++s) mbar_init(smem_u32(&full[g][s]), 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  const T* x = static_cast<const T*>(p.x);
+  const long long first = static_cast<long long>(blockIdx.x) * kGroups + group;
+  const long long stride = static_cast<long long>(gridDim.x) * kGroups;
+  if (t == 0) {
+    long long row = first;
+    for (int s = 0; s < slots && row < p.rows; ++s, row += stride)
+      ring.fill(s, x + row * p.ld_x, nullptr);
+  }
+  params_to_shared<T, VEC>(p.weight, p.params_f32, 1.0f, p.cols, w_sm);
+  params_to_shared<T, VEC>(p.bias, p.params_f32, 0.0f, p.cols, b_sm);
+  __syncthreads();
+  const float inv = 1.0f / static_cast<float>(p.cols);
+  int it = 0;      // rows of the group so far
+  for (long long row = first; row < p.rows; row += ROWS * stride, it += ROWS) {
+    // rows past the last are computed on what their buffers hold, not stored
+    const T* xr[ROWS];
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+      if (row + q * stride < p.rows) ring.wait(it + q);
+      xr[q] = reinterpret_cast<const T*>(ring.slot(it + q));
+    }
+    float2 v[ROWS][N][VEC / 2];
+    float2 acc[ROWS];
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) acc[q] = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * TPR + t) * VEC;
+      if (c < p.cols) {
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+          load_pairs<T, VEC>(xr[q] + c, v[q][i]);
+#pragma unroll
+          for (int j = 0; j < VEC / 2; ++j) acc[q] = __fadd2_rn(acc[q], v[q][i][j]);
+        }
+      }
+    }
+    float mean[ROWS], rstd[ROWS];
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) mean[q] = acc[q].x + acc[q].y;
+    group_reduce<TPR, ROWS, false>(mean, red[group][0], group);
+    // past the barrier every thread of the group has its part in registers
+    if (t == 0) {
+#pragma unroll
+      for (int q = 0; q < ROWS; ++q) {
+        const long long next = row + (q + slots) * stride;
+        if (next < p.rows) ring.fill(it + q + slots, x + next * p.ld_x, nullptr);
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+      mean[q] *= inv;
+      acc[q] = make_float2(0.0f, 0.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if ((i * TPR + t) * VEC < p.cols) {
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+          const float2 shift = pair_of(-mean[q]);
+#pragma unroll
+          for (int j = 0; j < VEC / 2; ++j) {
+            v[q][i][j] = __fadd2_rn(v[q][i][j], shift);
+            acc[q] = __ffma2_rn(v[q][i][j], v[q][i][j], acc[q]);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) rstd[q] = acc[q].x + acc[q].y;
+    group_reduce<TPR, ROWS, false>(rstd, red[group][1], group);
+    float amax[ROWS];
+#pragma unroll
+    for (int q = 0; q < ROWS; ++q) {
+      rstd[q] = __frsqrt_rn(fmaf(rstd[q], inv, p.eps));
+      amax[q] = 0.0f;
+      if (t == 0 && row + q * stride < p.rows) {
+        if (p.mean != nullptr) p.mean[row + q * stride] = mean[q];
+        if (p.rstd != nullptr) p.rstd[row + q * stride] = rstd[q];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * TPR + t) * VEC;
+      if (c < p.cols) {
+        float2 w[VEC / 2], b[VEC / 2];
+        shared_pairs<VEC>(w_sm, i * TPR + t, p.cols, w);
+        shared_pairs<VEC>(b_sm, i * TPR + t, p.cols, b);
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+          const float2 scale = pair_of(rstd[q]);
+#pragma unroll
+          for (int j = 0; j < VEC / 2; ++j) {
+            float2& o = v[q][i][j];
+            o = __ffma2_rn(__fmul2_rn(o, scale), w[j], b[j]);
+            if (Q) amax[q] = fmaxf(fmaxf(amax[q], fabsf(o.x)), fabsf(o.y));
+          }
+          if (p.y != nullptr && row + q * stride < p.rows) {
+            float f[VEC];
+#pragma unroll
+            for (int j = 0; j < VEC / 2; ++j) {
+              f[2 * j] = v[q][i][j].x;
+              f[2 * j + 1] = v[q][i][j].y;
+            }
+            norm_store<T, VEC>(static_cast<T*>(p.y) + (row + q * stride) * p.cols + c, f);
+          }
+        }
+      }
+    }
+    if constexpr (Q) {
+      group_reduce<TPR, ROWS, true>(amax, red[group][2], group);
+      auto codes = [&](auto fmt) {
+        constexpr int kFmt = decltype(fmt)::value;
+#pragma unroll
+        for (int q = 0; q < ROWS; ++q) {
+          if (row + q * stride >= p.rows) continue;
+          const float s = __fdiv_rn(fmaxf(amax[q], kGuardAmax), Fp8Out<kFmt>::kMax);
+          const float2 r = pair_of(__frcp_rn(s));
+          if (t == 0) p.scales[row + q * stride] = s;
+          uint8_t* qr = p.q + (row + q * stride) * p.cols;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const int c = (i * TPR + t) * VEC;
+            if (c < p.cols) {
+              uint32_t o[VEC / 4];
+#pragma unroll
+              for (int j = 0; j < VEC / 4; ++j) {
+                const float2 lo = __fmul2_rn(v[q][i][2 * j], r);
+                const float2 hi = __fmul2_rn(v[q][i][2 * j + 1], r);
+                o[j] = cvt_pair<kFmt>(lo.x, lo.y) | (cvt_pair<kFmt>(hi.x, hi.y) << 16);
+              }
+              store_codes<VEC>(qr + c, o);
+            }
+          }
+        }
+      };
+      if (p.q_fmt == SFP8_E5M2) codes(std::integral_constant<int, SFP8_E5M2>{});
+      else codes(std::integral_constant<int, SFP8_E4M3>{});
+    }
+  }
+  if (t == 0) ring.drain(p.rows > first ? static_cast<int>((p.rows - first + stride - 1) / stride) : 0);
 }
 
 // ------------------------------------------------------------------ backward
@@ -435,6 +749,163 @@ __global__ void __launch_bounds__(TPR > 256 ? TPR : 256)
       }
     }
   }
+}
+
+// Stream form: x and dy of a row come through the ring and are read from it
+// twice, before the reduction (the sums) and after it (dx), which leaves the
+// registers to the running sums.  A slot is refilled after the next row's
+// barrier, when every thread has finished with it.  With c = x - mean:
+//     sums      A = sum g / C,   B = rstd * sum (g c) / C
+//     dx        = g rstd - A rstd - c (B rstd^2)
+// At the end the block adds its groups' sums in group order: one partial sum
+// a block.
+template <typename T, int VEC, int TPR, int N, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1)
+    layernorm_backward_stream_kernel(const NormGradParams p, int slots) {
+  extern __shared__ __align__(128) uint8_t norm_smem[];
+  static_assert(THREADS % TPR == 0, "whole row groups");
+  constexpr int kGroups = THREADS / TPR;
+  __shared__ uint64_t full[kGroups][kNormMaxSlots];
+  __shared__ int abort_flag;
+  // two sets, by row: a thread is at most one barrier behind
+  __shared__ __align__(16) float2 red[kGroups][2][TPR / 32];
+  grid_dependents_launch();
+  const int group = threadIdx.x / TPR;
+  const int t = threadIdx.x % TPR;
+  float* w_sm = reinterpret_cast<float*>(norm_smem);
+  const uint32_t bytes = static_cast<uint32_t>(p.cols * sizeof(T));
+  uint8_t* rings = norm_smem + 4ll * p.cols;
+  const NormRing<2> ring{rings + static_cast<size_t>(group) * slots * 2 * bytes, full[group],
+                         &abort_flag, bytes, slots};
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < kGroups; ++g)
+      for (int s = 0; s < slots; ++s) mbar_init(smem_u32(&full[g][s]), 1);
+    abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  grid_dependency_wait();
+  const T* x = static_cast<const T*>(p.x);
+  const T* dy = static_cast<const T*>(p.dy);
+  const long long first = static_cast<long long>(blockIdx.x) * kGroups + group;
+  const long long stride = static_cast<long long>(gridDim.x) * kGroups;
+  if (t == 0) {
+    long long row = first;
+    for (int s = 0; s < slots && row < p.rows; ++s, row += stride)
+      ring.fill(s, x + row * p.ld_x, dy + row * p.ld_dy);
+  }
+  params_to_shared<T, VEC>(p.weight, p.params_f32, 1.0f, p.cols, w_sm);
+  __syncthreads();
+  float2 dw[N][VEC / 2], db[N][VEC / 2];
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) dw[i][j] = db[i][j] = make_float2(0.0f, 0.0f);
+  const float inv = 1.0f / static_cast<float>(p.cols);
+  int it = 0;      // rows of the group so far
+  float mean = 0.0f, rstd = 0.0f;
+  if (first < p.rows) {
+    mean = p.mean[first];
+    rstd = p.rstd[first];
+  }
+  for (long long row = first; row < p.rows; row += stride, ++it) {
+    float mean_n = 0.0f, rstd_n = 0.0f;
+    if (row + stride < p.rows) {
+      mean_n = p.mean[row + stride];
+      rstd_n = p.rstd[row + stride];
+    }
+    ring.wait(it);
+    const T* xr = reinterpret_cast<const T*>(ring.slot(it));
+    const T* dr = xr + p.cols;
+    const float2 shift = pair_of(-mean), scale = pair_of(rstd);
+    float2 sg = make_float2(0.0f, 0.0f), sgc = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * TPR + t) * VEC;
+      if (c < p.cols) {
+        float2 xc[VEC / 2], d[VEC / 2], w[VEC / 2];
+        load_pairs<T, VEC>(xr + c, xc);
+        load_pairs<T, VEC>(dr + c, d);
+        shared_pairs<VEC>(w_sm, i * TPR + t, p.cols, w);
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+          xc[j] = __fadd2_rn(xc[j], shift);
+          dw[i][j] = __ffma2_rn(d[j], __fmul2_rn(xc[j], scale), dw[i][j]);
+          db[i][j] = __fadd2_rn(db[i][j], d[j]);
+          const float2 g = __fmul2_rn(d[j], w[j]);
+          sg = __fadd2_rn(sg, g);
+          sgc = __ffma2_rn(g, xc[j], sgc);
+        }
+      }
+    }
+    float2 sums = make_float2(sg.x + sg.y, sgc.x + sgc.y);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      sums.x += __shfl_xor_sync(0xffffffffu, sums.x, o);
+      sums.y += __shfl_xor_sync(0xffffffffu, sums.y, o);
+    }
+    float2(&rd)[TPR / 32] = red[group][it & 1];
+    if (t % 32 == 0) rd[t / 32] = sums;
+    named_barrier_sync(1 + group, TPR);
+    // the group has finished with the previous row: refill its slot
+    if (t == 0 && it > 0 && row + (slots - 1) * stride < p.rows) {
+      const long long next = row + (slots - 1) * stride;
+      ring.fill(it - 1 + slots, x + next * p.ld_x, dy + next * p.ld_dy);
+    }
+    if (p.dx != nullptr) {
+      float2 total = rd[0];
+#pragma unroll
+      for (int i = 1; i < TPR / 32; ++i) total = __fadd2_rn(total, rd[i]);
+      const float a = total.x * inv, b = total.y * inv * rstd;
+      const float2 ka = pair_of(-a * rstd), kb = pair_of(-b * rstd * rstd);
+      T* out = static_cast<T*>(p.dx) + row * p.cols;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = (i * TPR + t) * VEC;
+        if (c < p.cols) {
+          float2 xc[VEC / 2], d[VEC / 2], w[VEC / 2];
+          load_pairs<T, VEC>(xr + c, xc);
+          load_pairs<T, VEC>(dr + c, d);
+          shared_pairs<VEC>(w_sm, i * TPR + t, p.cols, w);
+          float f[VEC];
+#pragma unroll
+          for (int j = 0; j < VEC / 2; ++j) {
+            const float2 u = __ffma2_rn(__fmul2_rn(d[j], w[j]), scale, ka);
+            const float2 o = __ffma2_rn(__fadd2_rn(xc[j], shift), kb, u);
+            f[2 * j] = o.x;
+            f[2 * j + 1] = o.y;
+          }
+          norm_store<T, VEC>(out + c, f);
+        }
+      }
+    }
+    mean = mean_n;
+    rstd = rstd_n;
+  }
+  if (t == 0) ring.drain(it);
+  // The rings are done with (every copy has been waited for): the groups add
+  // their sums into them in order.
+  float* total = reinterpret_cast<float*>(rings);
+  for (int g = 0; g < kGroups; ++g) {
+    __syncthreads();
+    if (g != group) continue;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = (i * TPR + t) * VEC;
+      if (c >= p.cols) continue;
+#pragma unroll
+      for (int j = 0; j < VEC / 2; ++j) {
+        float2* a = reinterpret_cast<float2*>(total + c + 2 * j);
+        float2* b = reinterpret_cast<float2*>(total + p.cols + c + 2 * j);
+        *a = g == 0 ? dw[i][j] : __fadd2_rn(*a, dw[i][j]);
+        *b = g == 0 ? db[i][j] : __fadd2_rn(*b, db[i][j]);
+      }
+    }
+  }
+  __syncthreads();
+  float* part = p.partial + static_cast<long long>(blockIdx.x) * 2 * p.cols;
+  for (int c = threadIdx.x * 4; c < 2 * p.cols; c += THREADS * 4)
+    *reinterpret_cast<float4*>(part + c) = *reinterpret_cast<const float4*>(total + c);
 }
 
 // Rows of any length: dx with two sweeps of the row, one row per block.

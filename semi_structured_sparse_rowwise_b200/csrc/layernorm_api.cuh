@@ -7,6 +7,9 @@
 namespace sfp8 {
 namespace {
 
+// Shared memory a stream kernel may use.
+constexpr int kNormSmemBudget = 224 * 1024;
+
 // ------------------------------------------------------------------ forward
 
 template <typename T, int VEC, int TPR, int N, bool Q>
@@ -18,16 +21,92 @@ sfp8_status launch_norm_rows(const NormParams& p, cudaStream_t st) {
                           dim3(threads), 0, st, p);
 }
 
+// Row buffers of a row group: what is left of the block's shared memory after
+// the parameters, at most eight rows.
+int norm_slots(int groups, int params, int cols, int parts, int row_bytes) {
+  const int left = kNormSmemBudget - params * cols * 4;
+  const int s = left / (groups * parts * row_bytes);
+  return s < kNormMaxSlots ? s : kNormMaxSlots;
+}
+
+// Co-resident blocks of a persistent kernel on the device (queried once a
+// slot; `smem` is the same for every launch that uses the slot).
+template <typename Kernel>
+sfp8_status norm_resident(DeviceInfo* dev, int slot, Kernel kern, int threads, int smem,
+                          int* blocks) {
+  std::lock_guard<std::mutex> lock(g_mutex);
+  if (dev->norm_blocks[slot] == 0) {
+    int occ = 0;
+    if ((smem > 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          smem) != cudaSuccess) ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem) != cudaSuccess ||
+        occ < 1) {
+      cudaGetLastError();
+      return SFP8_ERR_CUDA;
+    }
+    dev->norm_blocks[slot] = occ;
+  }
+  *blocks = dev->norm_blocks[slot] * dev->num_sms;
+  return SFP8_OK;
+}
+
+// Blocks of a stream kernel: one a SM, or as many as leave every row group the
+// same number of rows, give or take one.
+int norm_stream_blocks(const DeviceInfo* dev, int per_block, int64_t rows) {
+  const int64_t groups = static_cast<int64_t>(per_block) * dev->num_sms;
+  const int64_t each = (rows + groups - 1) / groups;
+  const int64_t used = (rows + each - 1) / each;
+  return static_cast<int>((used + per_block - 1) / per_block);
+}
+
+// threads: of a block, per_block row groups; params, parts: fp32 parameter
+// vectors and rows (x; x and dy) in shared memory.
+template <typename Kernel, typename P>
+sfp8_status launch_norm_stream(DeviceInfo* dev, int slot, Kernel kern, int threads,
+                               int per_block, const P& p, int params, int parts, int row_bytes,
+                               cudaStream_t st) {
+  const int slots = norm_slots(per_block, params, p.cols, parts, row_bytes);
+  if (slots < 2) return SFP8_ERR_UNSUPPORTED_SHAPE;   // no such width is sent here
+  {
+    std::lock_guard<std::mutex> lock(g_mutex);
+    if (dev->norm_blocks[slot] == 0) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               kNormSmemBudget) != cudaSuccess) {
+        cudaGetLastError();
+        return SFP8_ERR_CUDA;
+      }
+      dev->norm_blocks[slot] = 1;
+    }
+  }
+  return launch_dependent(
+      kern, dim3(static_cast<unsigned>(norm_stream_blocks(dev, per_block, p.rows))),
+      dim3(threads),
+      static_cast<size_t>(norm_stream_smem(per_block, params, p.cols, parts, row_bytes, slots)),
+      st, p, slots);
+}
+
 // 16-byte vectors.  Few rows (a decode step, fewer than two a SM): as many
 // threads as vectors, so that the chain of one load, three reductions and one
-// store is all a row takes.  Many rows: up to four vectors a thread, so that
-// a row's reductions span fewer warps and each warp has more bytes in flight.
+// store is all a row takes.  Many rows (eight a SM and more): the stream
+// kernel (8192 rows of 4096 bf16 to codes: 32 us, the row kernel with four
+// vectors a thread 43 us), with as many row groups as its registers allow.
 template <typename T, bool Q>
-sfp8_status launch_norm_vec(const NormParams& p, int num_sms, cudaStream_t st) {
+sfp8_status launch_norm_vec(DeviceInfo* dev, int kind, const NormParams& p, cudaStream_t st) {
   constexpr int V = InputTraits<T>::kPerVec;
   const int nvec = p.cols / V;
+  const int s0 = kind * 12 + (Q ? 4 : 0);
   if (nvec <= 32) return launch_norm_rows<T, V, 32, 1, Q>(p, st);
-  if (p.rows < 2ll * num_sms) {
+  if (nvec > 64 && nvec <= 1024 && p.rows >= 8ll * dev->num_sms) {
+    const int bytes = p.cols * static_cast<int>(sizeof(T));
+    auto go = [&](int slot, auto kern, int threads, int per_block) {
+      return launch_norm_stream(dev, s0 + slot, kern, threads, per_block, p, 2, 1, bytes, st);
+    };
+    if (nvec <= 128) return go(0, layernorm_stream_kernel<T, V, 128, 1, 2, 1024, Q>, 1024, 8);
+    if (nvec <= 256) return go(1, layernorm_stream_kernel<T, V, 128, 2, 2, 768, Q>, 768, 6);
+    if (nvec <= 512) return go(2, layernorm_stream_kernel<T, V, 128, 4, 2, 512, Q>, 512, 4);
+    return go(3, layernorm_stream_kernel<T, V, 256, 4, 2, 512, Q>, 512, 2);
+  }
+  if (p.rows < 2ll * dev->num_sms) {
     if (nvec <= 128) return launch_norm_rows<T, V, 128, 1, Q>(p, st);
     if (nvec <= 512) return launch_norm_rows<T, V, 512, 1, Q>(p, st);
     if (nvec <= 1024) return launch_norm_rows<T, V, 1024, 1, Q>(p, st);
@@ -53,23 +132,25 @@ sfp8_status launch_norm_scalar(const NormParams& p, cudaStream_t st) {
                           dim3(static_cast<unsigned>(p.rows)), dim3(1024), 0, st, p);
 }
 
+// kind: the type's index, for the cached occupancies.
 template <typename T>
-sfp8_status launch_norm(const NormParams& p, bool vec, int num_sms, cudaStream_t st) {
-  if (p.q != nullptr) return launch_norm_vec<T, true>(p, num_sms, st);
-  if (vec) return launch_norm_vec<T, false>(p, num_sms, st);
+sfp8_status launch_norm(DeviceInfo* dev, int kind, const NormParams& p, bool vec,
+                        cudaStream_t st) {
+  if (p.q != nullptr) return launch_norm_vec<T, true>(dev, kind, p, st);
+  if (vec) return launch_norm_vec<T, false>(dev, kind, p, st);
   return launch_norm_scalar<T>(p, st);
 }
 
 // ------------------------------------------------------------------ backward
 
 // Row groups the backward pass may use (each leaves one partial sum of 2 cols
-// floats): two a SM, and for many short rows up to 16 a SM as long as every
+// floats): three a SM, and for many short rows up to 16 a SM as long as every
 // group still has 16 rows, which keeps the partial sums' traffic a small
 // part of the inputs'.
 int64_t norm_groups(int64_t rows, int num_sms) {
   int64_t g = rows / 16;
   if (g > 16ll * num_sms) g = 16ll * num_sms;
-  if (g < 2ll * num_sms) g = 2ll * num_sms;
+  if (g < 3ll * num_sms) g = 3ll * num_sms;
   return g < rows ? g : rows;
 }
 
@@ -78,23 +159,21 @@ sfp8_status launch_norm_grad_rows(DeviceInfo* dev, int slot, NormGradParams& p, 
   auto kern = layernorm_backward_kernel<T, VEC, TPR, N>;
   constexpr int threads = TPR == 32 ? 256 : TPR;
   constexpr int per_block = TPR == 32 ? 8 : 1;
-  {
-    std::lock_guard<std::mutex> lock(g_mutex);
-    if (dev->norm_blocks[slot] == 0) {
-      int occ = 0;
-      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, 0) != cudaSuccess ||
-          occ < 1) {
-        cudaGetLastError();
-        return SFP8_ERR_CUDA;
-      }
-      dev->norm_blocks[slot] = occ;
-    }
-  }
+  int blocks = 0;
+  const sfp8_status s = norm_resident(dev, slot, kern, threads, 0, &blocks);
+  if (s != SFP8_OK) return s;
   // one wave of co-resident blocks
-  const int64_t most = static_cast<int64_t>(dev->norm_blocks[slot]) * dev->num_sms * per_block;
-  if (p.groups > most) p.groups = static_cast<int>(most);
+  if (p.groups > static_cast<int64_t>(blocks) * per_block) p.groups = blocks * per_block;
   return launch_dependent(kern, dim3(static_cast<unsigned>((p.groups + per_block - 1) / per_block)),
                           dim3(threads), 0, st, p);
+}
+
+template <typename T, typename Kernel>
+sfp8_status launch_norm_grad_stream(DeviceInfo* dev, int slot, Kernel kern, int threads,
+                                    int per_block, NormGradParams& p, cudaStream_t st) {
+  p.groups = norm_stream_blocks(dev, per_block, p.rows);   // one partial sum a block
+  return launch_norm_stream(dev, slot, kern, threads, per_block, p, 1, 2,
+                            p.cols * static_cast<int>(sizeof(T)), st);
 }
 
 // Rows too long for the registers: dx by rows, the sums by columns.
@@ -120,15 +199,18 @@ template <typename T>
 sfp8_status launch_norm_grad(DeviceInfo* dev, int kind, NormGradParams& p, bool vec, bool sums,
                              cudaStream_t st) {
   constexpr int V = InputTraits<T>::kPerVec;
-  const int s0 = kind * 10;
+  const int s0 = 36 + kind * 8;
   if (vec) {
     const int nvec = p.cols / V;
     if (nvec <= 32) return launch_norm_grad_rows<T, V, 32, 1>(dev, s0, p, st);
     if (nvec <= 64) return launch_norm_grad_rows<T, V, 32, 2>(dev, s0 + 1, p, st);
-    if (nvec <= 128) return launch_norm_grad_rows<T, V, 128, 1>(dev, s0 + 2, p, st);
-    if (nvec <= 256) return launch_norm_grad_rows<T, V, 256, 1>(dev, s0 + 3, p, st);
-    if (nvec <= 512) return launch_norm_grad_rows<T, V, 512, 1>(dev, s0 + 4, p, st);
-    if (nvec <= 1024) return launch_norm_grad_rows<T, V, 512, 2>(dev, s0 + 5, p, st);
+    auto go = [&](int slot, auto kern, int threads, int per_block) {
+      return launch_norm_grad_stream<T>(dev, s0 + slot, kern, threads, per_block, p, st);
+    };
+    if (nvec <= 128) return go(2, layernorm_backward_stream_kernel<T, V, 128, 1, 768>, 768, 6);
+    if (nvec <= 256) return go(3, layernorm_backward_stream_kernel<T, V, 128, 2, 640>, 640, 5);
+    if (nvec <= 512) return go(4, layernorm_backward_stream_kernel<T, V, 128, 4, 512>, 512, 4);
+    if (nvec <= 1024) return go(5, layernorm_backward_stream_kernel<T, V, 256, 4, 512>, 512, 2);
   } else {
     if (p.cols <= 1024) return launch_norm_grad_rows<T, 1, 128, 8>(dev, s0 + 6, p, st);
     if (p.cols <= 4096) return launch_norm_grad_rows<T, 1, 512, 8>(dev, s0 + 7, p, st);
@@ -191,9 +273,9 @@ sfp8_status sfp8_layernorm(const void* x, sfp8_dtype x_dtype, int64_t rows, int6
   p.rstd = rstd;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   switch (x_dtype) {
-    case SFP8_BF16: return launch_norm<__nv_bfloat16>(p, vec, dev->num_sms, st);
-    case SFP8_F16: return launch_norm<__half>(p, vec, dev->num_sms, st);
-    default: return launch_norm<float>(p, vec, dev->num_sms, st);
+    case SFP8_BF16: return launch_norm<__nv_bfloat16>(dev, 0, p, vec, st);
+    case SFP8_F16: return launch_norm<__half>(dev, 1, p, vec, st);
+    default: return launch_norm<float>(dev, 2, p, vec, st);
   }
 }
 

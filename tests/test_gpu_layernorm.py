@@ -82,6 +82,17 @@ def test_forward(rows, cols, dtype):
     check_forward(y, mean, rstd, x, w, b, dtype)
 
 
+# eight rows a SM and more: the persistent kernel, at every class of width and
+# with a last row that leaves some row groups short
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [264, 520, 1000, 1024, 1032, 2048, 2056, 3000, 4096, 5000, 8192])
+@pytest.mark.parametrize("rows", [1187, 2500])
+def test_forward_many_rows(rows, cols, dtype):
+    x, w, b = inputs(rows, cols, dtype, rows + cols)
+    y, mean, rstd = S.sfp8_layernorm(x, w, b, EPS)
+    check_forward(y, mean, rstd, x, w, b, dtype)
+
+
 def fp8_half_step(v, fmt):
     """Half the spacing of the format's values at magnitude v."""
     bits, low = (3, -6) if fmt == "e4m3" else (2, -14)
@@ -91,8 +102,9 @@ def fp8_half_step(v, fmt):
 
 @pytest.mark.parametrize("fmt", ["e4m3", "e5m2"])
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("cols", [16, 48, 512, 1024, 4096, 8208, 16384, 40960])
-@pytest.mark.parametrize("rows", [1, 16, 310])
+@pytest.mark.parametrize("rows,cols", [(r, c) for r in (1, 16, 310)
+                                       for c in (16, 48, 512, 1024, 4096, 8208, 16384, 40960)]
+                         + [(r, c) for r in (1184, 3001) for c in (528, 1024, 2064, 4096, 7680)])
 def test_codes(rows, cols, dtype, fmt):
     x, w, b = inputs(rows, cols, dtype, rows + cols)
     y = torch.empty_like(x)
@@ -184,7 +196,7 @@ def check_backward(got, dy, x, w, mean, rstd, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("cols", [1, 3, 8, 200, 256, 512, 1000, 1003, 1024, 2048, 4096, 4099, 5001,
                                   8192, 9000, 16384])
-@pytest.mark.parametrize("rows", [1, 37, 700])
+@pytest.mark.parametrize("rows", [1, 37, 700, 1999])
 def test_backward(rows, cols, dtype):
     x, w, b = inputs(rows, cols, dtype, rows + cols)
     _, mean, rstd = S.sfp8_layernorm(x, w, b, EPS)
