@@ -617,10 +617,15 @@ def _quant_linear(name, x, a_dtype, packed, w_dtype, s_w, n, k, bias, out, works
 # object and ctypes pointer objects alone take that long.
 
 
+_FN = {}
+
+
 def _run(name, device, *args):
     """Calls the library on `device`'s current stream (the last argument) and
     raises on a status other than OK."""
-    fn = getattr(load_library(), name)
+    fn = _FN.get(name)
+    if fn is None:
+        fn = _FN[name] = getattr(load_library(), name)
     index = device.index
     if torch._C._cuda_getDevice() == index:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -633,6 +638,17 @@ def _run(name, device, *args):
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _like(x, t, what, dtype):
+    """A contiguous output of x's shape: given (checked) or new (empty_like is
+    the cheaper call where it gives that)."""
+    if t is None:
+        if x.is_contiguous():
+            return torch.empty_like(x, dtype=dtype)
+        return torch.empty(x.shape, dtype=dtype, device=x.device)
+    _tensor(t, what, x.shape, dtype, x.device)
+    return t
 
 
 def _fp8(dtype):
@@ -698,8 +714,11 @@ def _codes(a_q, s_a, k):
 
 
 def _workspace(ws, device):
-    """Address and size of a caller's workspace."""
-    return ws.data_ptr(), _ws_bytes(ws, device)
+    """Address and size of a caller's workspace (any dtype), which must be a
+    contiguous CUDA tensor on `device`."""
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on %s" % (device,))
+    return ws.data_ptr(), ws.nbytes
 
 
 def _new_workspace(query, sizes, device):
@@ -774,7 +793,7 @@ def sfp8_gated_linear_quant(x, a_dtype, packed, w_dtype, s_w, n, k, act="silu", 
     m, dev = x.shape[0], x.device
     _gated_weight(n, k, packed, s_w, bias, dev)
     out = _out(out, "out", (m, n), torch.bfloat16, dev)
-    a_q = _out(a_q, "a_q", (m, k), torch.uint8, dev)
+    a_q = _like(x, a_q, "a_q", torch.uint8)
     s_a = _out(s_a, "s_a", (m,), torch.float32, dev)
     if workspace is None:
         workspace = new_gated_quant_workspace(m, n, k, dev)
@@ -896,7 +915,7 @@ def sfp8_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, mean=None, rst
     """Layer norm of x [rows, cols] bf16/f16/f32 (unit column stride), weight
     and bias [cols] of x's dtype or float32: returns (y of x's dtype, mean
     [rows], rstd [rows] float32)."""
-    out = _out(out, "out", x.shape, x.dtype, x.device)
+    out = _like(x, out, "out", x.dtype)
     mean, rstd = _row_vectors(x.shape[0], x.device, ("mean", mean), ("rstd", rstd))
     _norm_forward(x, weight, bias, eps, out, None, "e4m3", None, mean, rstd)
     return out, mean, rstd
@@ -907,7 +926,7 @@ def sfp8_layernorm_quant(x, weight=None, bias=None, eps=1e-5, q_dtype="e4m3", q=
     """Layer norm of x straight to row-wise FP8 codes, the input of the linear
     and the gated block: returns (q [rows, cols] uint8, scales, mean, rstd
     [rows] float32).  A given `out` also receives y in x's dtype."""
-    q = _out(q, "q", x.shape, torch.uint8, x.device)
+    q = _like(x, q, "q", torch.uint8)
     if out is not None:
         _tensor(out, "out", x.shape, x.dtype, x.device)
     scales, mean, rstd = _row_vectors(x.shape[0], x.device, ("scales", scales), ("mean", mean),
@@ -936,7 +955,7 @@ def sfp8_layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, db
     rows, cols = x.shape
     _tensor(mean, "mean", (rows,), torch.float32, dev)
     _tensor(rstd, "rstd", (rows,), torch.float32, dev)
-    dx = _out(dx, "dx", (rows, cols), x.dtype, dev)
+    dx = _like(x, dx, "dx", x.dtype)
     dweight = _out(dweight, "dweight", (cols,), torch.float32, dev)
     dbias = _out(dbias, "dbias", (cols,), torch.float32, dev)
     if workspace is None:

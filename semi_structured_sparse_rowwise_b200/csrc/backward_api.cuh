@@ -252,7 +252,7 @@ sfp8_status launch_prologue(DeviceInfo* dev, const BackwardPlan& bp, const Backw
                          p.blocks[3];
   if (blocks == 0) return SFP8_OK;
   return launch_dependent(backward_prologue_kernel, dim3(static_cast<unsigned>(blocks)),
-                          dim3(256), 0, st, p);
+                          dim3(256), sums ? 8 * kColSumCols * sizeof(float) : 0, st, p);
 }
 
 // dx and dw from dz [m, rows] (row stride ld, 16-byte aligned, ld a multiple
@@ -302,7 +302,7 @@ sfp8_status launch_linear_grads(DeviceInfo* dev, const BackwardPlan& bp, const B
       pr.idesc = make_idesc_bf16(i == 1, true, kGgTileM, static_cast<uint32_t>(g.bn));
       if (pl.splits > 1) {
         jp.prob[at] = pr;
-        jp.blocks[at] = blocks_for(d_rows, 16, dev, 8);
+        jp.blocks[at] = blocks_for((d_rows + 15) / 16 * (c.k / 128), 1, dev, 8);
       }
     }
     prm.lag_rounds = g.lag_rounds;

@@ -78,7 +78,7 @@ struct GgProblem {
   __nv_bfloat16* d;       // [rows][cols]
   float* partial;         // [splits][rows][cols] fp32 (splits > 1)
   const float* row_scale; // [rows], divided out of D's rows; or null
-  int rows, cols;         // of D; cols a multiple of 16
+  int rows, cols;         // of D; cols a multiple of 128
   int m_tiles, n_tiles;
   int stages_total;       // ceil(contraction / 64)
   int splits;
@@ -444,7 +444,7 @@ struct JoinParams {
 };
 
 // D = the sum of the splits' partial sums, in split order, scaled and rounded
-// once (one thread per 8 columns); then, in blocks of their own, the bias
+// once (one thread per 8 columns; D's columns are a multiple of 128); then, in blocks of their own, the bias
 // gradient: 32 columns a block, each of 8 row lanes adding every eighth run,
 // the lanes added in order.
 __global__ void __launch_bounds__(256) backward_join_kernel(const __grid_constant__ JoinParams p) {
@@ -458,10 +458,13 @@ __global__ void __launch_bounds__(256) backward_join_kernel(const __grid_constan
     }
     const GgProblem& pr = p.prob[w];
     const long long plane = static_cast<long long>(pr.rows) * pr.cols;
-    // 16 rows of 16 vectors a block and step
-    for (long long r = static_cast<long long>(block) * 16 + threadIdx.x / 16; r < pr.rows;
-         r += static_cast<long long>(p.blocks[w]) * 16)
-    for (int c = threadIdx.x % 16 * 8; c < pr.cols; c += 128) {
+    // 16 rows x 128 columns a block and step
+    const int chunks = pr.cols / 128;
+    const int units = (pr.rows + 15) / 16 * chunks;
+    for (int u = block; u < units; u += p.blocks[w]) {
+      const long long r = static_cast<long long>(u / chunks) * 16 + threadIdx.x / 16;
+      const int c = u % chunks * 128 + threadIdx.x % 16 * 8;
+      if (r >= pr.rows) continue;
       float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       const float* src = pr.partial + r * pr.cols + c;
 #pragma unroll 4
@@ -632,7 +635,7 @@ __device__ __forceinline__ void copy_dy(const PrologueParams& p, int block) {
 // columns, 8 row lanes of 32 threads with 8 columns each.
 constexpr int kColSumCols = 256;
 __device__ __forceinline__ void sum_columns(const PrologueParams& p, int block,
-                                            float (&lanes)[8][kColSumCols]) {
+                                            float (*lanes)[kColSumCols]) {
   const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
   const long long c0 = static_cast<long long>(block / p.runs) * kColSumCols;
   const int run = block % p.runs;
@@ -671,9 +674,11 @@ __device__ __forceinline__ void sum_columns(const PrologueParams& p, int block,
   }
 }
 
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(256, 6)
     backward_prologue_kernel(const __grid_constant__ PrologueParams p) {
-  __shared__ float lanes[8][kColSumCols];
+  // only a launch that sums columns asks for the shared memory: without it,
+  // the gradient GEMM's blocks can be resident before this grid has drained
+  extern __shared__ __align__(16) float column_lanes[];
   grid_dependents_launch();
   grid_dependency_wait();
   int block = blockIdx.x;
@@ -682,7 +687,7 @@ __global__ void __launch_bounds__(256)
   if (part == 0) expand_weight(p, block);
   else if (part == 1) expand_rows(p, block);
   else if (part == 2) copy_dy(p, block);
-  else sum_columns(p, block, lanes);
+  else sum_columns(p, block, reinterpret_cast<float(*)[kColSumCols]>(column_lanes));
 }
 
 }  // namespace sfp8

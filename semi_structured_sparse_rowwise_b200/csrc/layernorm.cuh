@@ -995,24 +995,24 @@ __global__ void __launch_bounds__(256)
 }
 
 // dweight and dbias: the groups' partial sums added in order, 32 columns a
-// block, each of 8 row lanes adding every eighth group.
-__global__ void __launch_bounds__(256)
+// block, each of 32 row lanes adding every 32nd group.
+__global__ void __launch_bounds__(1024)
     layernorm_backward_join_kernel(const float* __restrict__ partial, int groups, int cols,
                                    float* __restrict__ dweight, float* __restrict__ dbias) {
-  __shared__ float sums[8][32];
+  __shared__ float sums[32][32];
   grid_dependents_launch();
   grid_dependency_wait();
   const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
   const long long col = static_cast<long long>(blockIdx.x) * 32 + tx;   // of 2 * cols
   float s = 0.0f;
   if (col < 2ll * cols) {
-#pragma unroll 8
-    for (int g = ty; g < groups; g += 8) s += partial[g * 2ll * cols + col];
+#pragma unroll 4
+    for (int g = ty; g < groups; g += 32) s += partial[g * 2ll * cols + col];
   }
   sums[ty][tx] = s;
   __syncthreads();
   if (ty == 0 && col < 2ll * cols) {
-    for (int j = 1; j < 8; ++j) s += sums[j][tx];
+    for (int j = 1; j < 32; ++j) s += sums[j][tx];
     if (col < cols) {
       if (dweight != nullptr) dweight[col] = s;
     } else if (dbias != nullptr) {

@@ -349,7 +349,7 @@ sfp8_status sfp8_layernorm_backward(const void* dy, int64_t ld_dy, const void* x
   }
   if (s != SFP8_OK || !sums) return s;
   return launch_dependent(layernorm_backward_join_kernel,
-                          dim3(static_cast<unsigned>((2 * cols + 31) / 32)), dim3(256), 0, st,
+                          dim3(static_cast<unsigned>((2 * cols + 31) / 32)), dim3(1024), 0, st,
                           static_cast<const float*>(p.partial), p.groups, p.cols, dweight, dbias);
 }
 
