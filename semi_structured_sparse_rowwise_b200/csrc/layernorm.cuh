@@ -21,7 +21,7 @@
 //                  N vectors of VEC elements each in registers, reduced by
 //                  warp shuffles and, for more than one warp, shared memory.
 //   stream kernel  many rows of 1 to 16 KB: one persistent block a SM with
-//                  two to eight row groups of 128 or 256 threads.  Each group
+//                  two to sixteen row groups of 64 to 256 threads.  Each group
 //                  has a ring of row buffers in shared memory that bulk
 //                  copies keep filled ahead, so that HBM streams through the
 //                  reductions' barriers; the parameters lie in shared memory
@@ -29,10 +29,10 @@
 //                  the latency of the reductions (a row per 256 threads in
 //                  scalar arithmetic issued 28 million warp instructions for
 //                  8192 rows of 4096 bf16 and took 47 us to codes): hence
-//                  packed fp32 pairs, few and wide threads a row, and in the
-//                  forward pass two rows a group at a time.  8192 x 4096
-//                  bf16: 32 us to codes (3.2 TB/s), 28 us to bf16 (4.7 TB/s),
-//                  46 us backward (4.4 TB/s).
+//                  packed fp32 pairs and few, wide threads a row.  8192 x
+//                  4096 bf16: 30 us to codes (3.3 TB/s), 26 us to bf16 (5.2
+//                  TB/s; 28 us with 128 threads a row), 44 us backward (4.5
+//                  TB/s).
 //   long kernels   rows that fit neither read them again from L2.
 // VEC elements make 16 bytes where base, row stride and width allow, else 1.
 //
@@ -419,34 +419,22 @@ __device__ __forceinline__ void params_to_shared(const void* p, int f32, float m
 
 __device__ __forceinline__ float2 pair_of(float v) { return make_float2(v, v); }
 
-// Sums (or maxima of magnitudes) over a row group of TPR threads, ROWS at a
-// time over one barrier of the group's own; `red` holds one value a warp and
-// row and is not written again before the group's next barrier.
-template <int TPR, int ROWS, bool kMax>
-__device__ __forceinline__ void group_reduce(float (&v)[ROWS], float (*red)[TPR / 32], int group) {
+// Sum (or maximum of magnitudes) over a row group of TPR threads, with one
+// barrier of the group's own; `red` holds one value a warp and is not written
+// again before the group's next barrier.
+template <int TPR, bool kMax>
+__device__ __forceinline__ float group_reduce(float v, float* red, int group) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-      const float t = __shfl_xor_sync(0xffffffffu, v[q], o);
-      v[q] = kMax ? fmaxf(v[q], t) : v[q] + t;
-    }
-  if (threadIdx.x % 32 == 0) {
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) red[q][threadIdx.x % TPR / 32] = v[q];
+  for (int o = 16; o > 0; o >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, v, o);
+    v = kMax ? fmaxf(v, t) : v + t;
   }
+  if (threadIdx.x % 32 == 0) red[threadIdx.x % TPR / 32] = v;
   named_barrier_sync(1 + group, TPR);
+  v = red[0];
 #pragma unroll
-  for (int q = 0; q < ROWS; ++q) {
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < TPR / 128; ++i) {
-      const float4 t = *reinterpret_cast<const float4*>(&red[q][4 * i]);
-      s = kMax ? fmaxf(s, fmaxf(fmaxf(t.x, t.y), fmaxf(t.z, t.w)))
-               : s + ((t.x + t.y) + (t.z + t.w));
-    }
-    v[q] = s;
-  }
+  for (int i = 1; i < TPR / 32; ++i) v = kMax ? fmaxf(v, red[i]) : v + red[i];
+  return v;
 }
 
 // Shared memory of a stream kernel: the parameters (`params` vectors of
@@ -457,9 +445,7 @@ __host__ __device__ constexpr int norm_stream_smem(int groups, int params, int c
 }
 
 // N vectors of VEC elements a thread: cols <= TPR * N * VEC, a multiple of VEC.
-// A group takes ROWS rows at a time: their reductions share the barriers and
-// overlap, and the parameters are read from shared memory once for all.
-template <typename T, int VEC, int TPR, int N, int ROWS, int THREADS, bool Q>
+template <typename T, int VEC, int TPR, int N, int THREADS, bool Q>
 __global__ void __launch_bounds__(THREADS, 1)
     layernorm_stream_kernel(const NormParams p, int slots) {
   extern __shared__ __align__(128) uint8_t norm_smem[];
@@ -467,7 +453,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr int kGroups = THREADS / TPR;
   __shared__ uint64_t full[kGroups][kNormMaxSlots];
   __shared__ int abort_flag;
-  __shared__ __align__(16) float red[kGroups][3][ROWS][TPR / 32];
+  __shared__ float red[kGroups][3][TPR / 32];
   grid_dependents_launch();
   const int group = threadIdx.x / TPR;
   const int t = threadIdx.x % TPR;
@@ -497,74 +483,45 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   const float inv = 1.0f / static_cast<float>(p.cols);
   int it = 0;      // rows of the group so far
-  for (long long row = first; row < p.rows; row += ROWS * stride, it += ROWS) {
-    // rows past the last are computed on what their buffers hold, not stored
-    const T* xr[ROWS];
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-      if (row + q * stride < p.rows) ring.wait(it + q);
-      xr[q] = reinterpret_cast<const T*>(ring.slot(it + q));
-    }
-    float2 v[ROWS][N][VEC / 2];
-    float2 acc[ROWS];
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) acc[q] = make_float2(0.0f, 0.0f);
+  for (long long row = first; row < p.rows; row += stride, ++it) {
+    ring.wait(it);
+    const T* xr = reinterpret_cast<const T*>(ring.slot(it));
+    float2 v[N][VEC / 2];
+    float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * TPR + t) * VEC;
       if (c < p.cols) {
+        load_pairs<T, VEC>(xr + c, v[i]);
 #pragma unroll
-        for (int q = 0; q < ROWS; ++q) {
-          load_pairs<T, VEC>(xr[q] + c, v[q][i]);
-#pragma unroll
-          for (int j = 0; j < VEC / 2; ++j) acc[q] = __fadd2_rn(acc[q], v[q][i][j]);
-        }
+        for (int j = 0; j < VEC / 2; ++j) acc = __fadd2_rn(acc, v[i][j]);
       }
     }
-    float mean[ROWS], rstd[ROWS];
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) mean[q] = acc[q].x + acc[q].y;
-    group_reduce<TPR, ROWS, false>(mean, red[group][0], group);
+    const float mean = group_reduce<TPR, false>(acc.x + acc.y, red[group][0], group) * inv;
     // past the barrier every thread of the group has its part in registers
-    if (t == 0) {
-#pragma unroll
-      for (int q = 0; q < ROWS; ++q) {
-        const long long next = row + (q + slots) * stride;
-        if (next < p.rows) ring.fill(it + q + slots, x + next * p.ld_x, nullptr);
-      }
-    }
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-      mean[q] *= inv;
-      acc[q] = make_float2(0.0f, 0.0f);
-    }
+    if (t == 0 && row + slots * stride < p.rows)
+      ring.fill(it + slots, x + (row + slots * stride) * p.ld_x, nullptr);
+    acc = make_float2(0.0f, 0.0f);
+    const float2 shift = pair_of(-mean);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if ((i * TPR + t) * VEC < p.cols) {
 #pragma unroll
-        for (int q = 0; q < ROWS; ++q) {
-          const float2 shift = pair_of(-mean[q]);
-#pragma unroll
-          for (int j = 0; j < VEC / 2; ++j) {
-            v[q][i][j] = __fadd2_rn(v[q][i][j], shift);
-            acc[q] = __ffma2_rn(v[q][i][j], v[q][i][j], acc[q]);
-          }
+        for (int j = 0; j < VEC / 2; ++j) {
+          v[i][j] = __fadd2_rn(v[i][j], shift);
+          acc = __ffma2_rn(v[i][j], v[i][j], acc);
         }
       }
     }
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) rstd[q] = acc[q].x + acc[q].y;
-    group_reduce<TPR, ROWS, false>(rstd, red[group][1], group);
-    float amax[ROWS];
-#pragma unroll
-    for (int q = 0; q < ROWS; ++q) {
-      rstd[q] = __frsqrt_rn(fmaf(rstd[q], inv, p.eps));
-      amax[q] = 0.0f;
-      if (t == 0 && row + q * stride < p.rows) {
-        if (p.mean != nullptr) p.mean[row + q * stride] = mean[q];
-        if (p.rstd != nullptr) p.rstd[row + q * stride] = rstd[q];
-      }
+    const float dev = group_reduce<TPR, false>(acc.x + acc.y, red[group][1], group);
+    const float rstd = __frsqrt_rn(fmaf(dev, inv, p.eps));
+    if (t == 0) {
+      if (p.mean != nullptr) p.mean[row] = mean;
+      if (p.rstd != nullptr) p.rstd[row] = rstd;
     }
+    float amax = 0.0f;
+    const float2 scale = pair_of(rstd);
+    T* yr = static_cast<T*>(p.y) + row * p.cols;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * TPR + t) * VEC;
@@ -573,50 +530,41 @@ __global__ void __launch_bounds__(THREADS, 1)
         shared_pairs<VEC>(w_sm, i * TPR + t, p.cols, w);
         shared_pairs<VEC>(b_sm, i * TPR + t, p.cols, b);
 #pragma unroll
-        for (int q = 0; q < ROWS; ++q) {
-          const float2 scale = pair_of(rstd[q]);
+        for (int j = 0; j < VEC / 2; ++j) {
+          float2& o = v[i][j];
+          o = __ffma2_rn(__fmul2_rn(o, scale), w[j], b[j]);
+          if (Q) amax = fmaxf(fmaxf(amax, fabsf(o.x)), fabsf(o.y));
+        }
+        if (p.y != nullptr) {
+          float f[VEC];
 #pragma unroll
           for (int j = 0; j < VEC / 2; ++j) {
-            float2& o = v[q][i][j];
-            o = __ffma2_rn(__fmul2_rn(o, scale), w[j], b[j]);
-            if (Q) amax[q] = fmaxf(fmaxf(amax[q], fabsf(o.x)), fabsf(o.y));
+            f[2 * j] = v[i][j].x;
+            f[2 * j + 1] = v[i][j].y;
           }
-          if (p.y != nullptr && row + q * stride < p.rows) {
-            float f[VEC];
-#pragma unroll
-            for (int j = 0; j < VEC / 2; ++j) {
-              f[2 * j] = v[q][i][j].x;
-              f[2 * j + 1] = v[q][i][j].y;
-            }
-            norm_store<T, VEC>(static_cast<T*>(p.y) + (row + q * stride) * p.cols + c, f);
-          }
+          norm_store<T, VEC>(yr + c, f);
         }
       }
     }
     if constexpr (Q) {
-      group_reduce<TPR, ROWS, true>(amax, red[group][2], group);
+      amax = group_reduce<TPR, true>(amax, red[group][2], group);
+      uint8_t* qr = p.q + row * p.cols;
       auto codes = [&](auto fmt) {
         constexpr int kFmt = decltype(fmt)::value;
+        const float s = __fdiv_rn(fmaxf(amax, kGuardAmax), Fp8Out<kFmt>::kMax);
+        const float2 r = pair_of(__frcp_rn(s));
+        if (t == 0) p.scales[row] = s;
 #pragma unroll
-        for (int q = 0; q < ROWS; ++q) {
-          if (row + q * stride >= p.rows) continue;
-          const float s = __fdiv_rn(fmaxf(amax[q], kGuardAmax), Fp8Out<kFmt>::kMax);
-          const float2 r = pair_of(__frcp_rn(s));
-          if (t == 0) p.scales[row + q * stride] = s;
-          uint8_t* qr = p.q + (row + q * stride) * p.cols;
+        for (int i = 0; i < N; ++i) {
+          const int c = (i * TPR + t) * VEC;
+          if (c < p.cols) {
+            uint32_t o[VEC / 4];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const int c = (i * TPR + t) * VEC;
-            if (c < p.cols) {
-              uint32_t o[VEC / 4];
-#pragma unroll
-              for (int j = 0; j < VEC / 4; ++j) {
-                const float2 lo = __fmul2_rn(v[q][i][2 * j], r);
-                const float2 hi = __fmul2_rn(v[q][i][2 * j + 1], r);
-                o[j] = cvt_pair<kFmt>(lo.x, lo.y) | (cvt_pair<kFmt>(hi.x, hi.y) << 16);
-              }
-              store_codes<VEC>(qr + c, o);
+            for (int j = 0; j < VEC / 4; ++j) {
+              const float2 lo = __fmul2_rn(v[i][2 * j], r), hi = __fmul2_rn(v[i][2 * j + 1], r);
+              o[j] = cvt_pair<kFmt>(lo.x, lo.y) | (cvt_pair<kFmt>(hi.x, hi.y) << 16);
             }
+            store_codes<VEC>(qr + c, o);
           }
         }
       };
@@ -624,7 +572,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       else codes(std::integral_constant<int, SFP8_E4M3>{});
     }
   }
-  if (t == 0) ring.drain(p.rows > first ? static_cast<int>((p.rows - first + stride - 1) / stride) : 0);
+  if (t == 0) ring.drain(it);
 }
 
 // ------------------------------------------------------------------ backward
