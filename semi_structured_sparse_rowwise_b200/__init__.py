@@ -1,4 +1,5 @@
-"""Row-wise scaled 2:4 sparse FP8 linear for B200 (sm_100a).
+"""Row-wise scaled 2:4 sparse FP8 linear for B200 (sm_100a), and the feed-forward
+sublayer around it: layer norm, gated block, backward passes.
 
 The compute path is libsfp8.so (C ABI, include/sfp8.h); this package holds
 its build script, a ctypes binding with the same function names, a layer
@@ -30,7 +31,8 @@ from .binding import (Sfp8Error, load_library, library_path, new_workspace,
                       new_layernorm_backward_workspace, sfp8_layernorm_backward,
                       sfp8_read_device_status, sfp8_selftest_timeout,
                       sfp8_status_string, sfp8_layout_version)
-from .layer import HostPipeline, SparseFp8Linear
+from .layer import (HostPipeline, SparseFp8FeedForward, SparseFp8GatedLinear,
+                    SparseFp8Linear)
 
 __all__ = [
     "Sfp8Error", "load_library", "library_path", "new_workspace",
@@ -54,5 +56,6 @@ __all__ = [
     "sfp8_layernorm", "sfp8_layernorm_quant", "new_layernorm_backward_workspace",
     "sfp8_layernorm_backward",
     "sfp8_read_device_status", "sfp8_selftest_timeout", "sfp8_status_string",
-    "sfp8_layout_version", "SparseFp8Linear", "HostPipeline",
+    "sfp8_layout_version", "SparseFp8Linear", "SparseFp8GatedLinear", "SparseFp8FeedForward",
+    "HostPipeline",
 ]

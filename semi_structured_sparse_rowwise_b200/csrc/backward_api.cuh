@@ -243,8 +243,9 @@ sfp8_status launch_prologue(DeviceInfo* dev, const BackwardPlan& bp, const Backw
   p.sums = reinterpret_cast<float*>(ws + bp.sums_off);
   p.runs = bp.runs;
   p.sums_by_16 = aligned(dy, 16) && ld_dy % 8 == 0;
-  if (c.dx != nullptr) p.blocks[0] = blocks_for((c.rows + 127) / 128 * (c.k / 128), 1, dev, 8);
-  if (c.dw != nullptr) p.blocks[1] = blocks_for((c.m + 127) / 128 * (c.k / 128), 1, dev, 8);
+  auto units = [&](int64_t r) { return (r + kExpandRows - 1) / kExpandRows * (c.k / 128); };
+  if (c.dx != nullptr) p.blocks[0] = blocks_for(units(c.rows), 1, dev, 8);
+  if (c.dw != nullptr) p.blocks[1] = blocks_for(units(c.m), 1, dev, 8);
   if (copy) p.blocks[2] = blocks_for(c.m, 1, dev, 8);
   if (sums)
     p.blocks[3] = static_cast<int>((c.rows + kColSumCols - 1) / kColSumCols) * bp.runs;

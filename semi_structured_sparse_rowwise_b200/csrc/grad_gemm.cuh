@@ -544,29 +544,33 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&b2);
 }
 
-// What[r, k] = bf16(dec(W_q[r, k]) * s_w[r]), dense, a 128 x 128 tile of the
-// packed weight at a time: every thread takes 8 pieces of 8 k (4 kept codes, 2
-// index nibbles), neighbouring threads neighbouring words of the tile and
+// Rows of the pieces that the expanding blocks take: half a packed tile, so
+// that medium sizes spread evenly over the device.
+constexpr int kExpandRows = 64;
+
+// What[r, k] = bf16(dec(W_q[r, k]) * s_w[r]), dense, half a 128 x 128 tile of
+// the packed weight at a time: every thread takes 4 pieces of 8 k (4 kept
+// codes, 2 index nibbles), neighbouring threads neighbouring words of the tile and
 // neighbouring 16-byte vectors of a row.  With s_w the one rounding (half a
 // bf16 step) is that of the operand; without it (null: the scales are in dz)
 // the codes are exact in bf16.
 __device__ __forceinline__ void expand_weight(const PrologueParams& p, int block) {
   const int ktiles = static_cast<int>(p.k / 128);
-  const long long tiles = (p.rows + 127) / 128 * ktiles;
-  for (long long t = block; t < tiles; t += p.blocks[0]) {
-    const long long nt = t / ktiles;
-    const uint8_t* tile = p.packed + t * 10240;
-    const long long row0 = nt * 128;
-    __nv_bfloat16* out = p.what + row0 * p.k + (t - nt * ktiles) * 128;
+  const int units = static_cast<int>((p.rows + kExpandRows - 1) / kExpandRows) * ktiles;
+  for (int u = block; u < units; u += p.blocks[0]) {
+    const int half = u / ktiles, kt = u - half * ktiles;   // 64-row group, k tile
+    const uint8_t* tile = p.packed + (static_cast<long long>(half / 2) * ktiles + kt) * 10240;
+    const long long tile0 = half / 2 * 128ll;
+    __nv_bfloat16* out = p.what + tile0 * p.k + kt * 128ll;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kExpandRows / 16; ++i) {
       const int item = i * 256 + threadIdx.x;
-      const int r = item / 16, j = item % 16;
-      if (row0 + r >= p.rows) continue;
+      const int r = half % 2 * kExpandRows + item / 16, j = item % 16;
+      if (tile0 + r >= p.rows) continue;
       const uint32_t vals = __ldg(reinterpret_cast<const uint32_t*>(
           tile + 64 * r + (((j / 4) ^ (r >> 1 & 3)) * 16) + (j % 4) * 4));
       const uint32_t meta = __ldg(tile + 8192 + 16 * r + j);
-      const float s = p.s_w != nullptr ? __ldg(p.s_w + row0 + r) : 1.0f;
+      const float s = p.s_w != nullptr ? __ldg(p.s_w + tile0 + r) : 1.0f;
       uint32_t w[4];
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
@@ -586,16 +590,16 @@ __device__ __forceinline__ void expand_weight(const PrologueParams& p, int block
 }
 
 // xhat[m, k] = bf16(dec(A_q[m, k]) * s_a[m]), or with s_a null the codes' own
-// values, 128 x 128 at a time as above.
+// values, 64 x 128 at a time as above.
 __device__ __forceinline__ void expand_rows(const PrologueParams& p, int block) {
   const int ktiles = static_cast<int>(p.k / 128);
-  const long long tiles = (p.m + 127) / 128 * ktiles;
-  for (long long t = block; t < tiles; t += p.blocks[1]) {
-    const long long mt = t / ktiles;
-    const long long row0 = mt * 128;
-    const long long at = row0 * p.k + (t - mt * ktiles) * 128;
+  const int units = static_cast<int>((p.m + kExpandRows - 1) / kExpandRows) * ktiles;
+  for (int u = block; u < units; u += p.blocks[1]) {
+    const int mt = u / ktiles;
+    const long long row0 = static_cast<long long>(mt) * kExpandRows;
+    const long long at = row0 * p.k + (u - mt * ktiles) * 128ll;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kExpandRows / 16; ++i) {
       const int item = i * 256 + threadIdx.x;
       const int r = item / 16, j = item % 16;
       if (row0 + r >= p.m) continue;
@@ -674,7 +678,7 @@ __device__ __forceinline__ void sum_columns(const PrologueParams& p, int block,
   }
 }
 
-__global__ void __launch_bounds__(256, 6)
+__global__ void __launch_bounds__(256)
     backward_prologue_kernel(const __grid_constant__ PrologueParams p) {
   // only a launch that sums columns asks for the shared memory: without it,
   // the gradient GEMM's blocks can be resident before this grid has drained

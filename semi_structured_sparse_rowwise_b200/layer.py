@@ -1,4 +1,5 @@
-"""The layer a user calls: a prepared 2:4 sparse FP8 weight and its forward.
+"""The layers a user calls: prepared 2:4 sparse FP8 weights, their forward and,
+from 8-bit activation checkpoints, their backward passes.
 
 Weight preparation (once, as the page "Add CUTLASS-based row-wise scaled
 sparse FP8 kernel", pytorch/ao pull request 1671, does at ``quantize_()`` time,
@@ -6,6 +7,14 @@ its items 1, 3 and 4): 2:4 magnitude prune -> row-wise FP8 quantisation ->
 2:4 compression.  Forward (per call): dynamic row-wise FP8 quantisation of the
 activation -> sparse FP8 GEMM with the scale/bias epilogue.  Every step is a
 kernel of libsfp8.so; torch only provides memory and streams.
+
+``SparseFp8Linear`` is one projection, ``SparseFp8GatedLinear`` the gate/up pair
+of a gated feed-forward block, ``SparseFp8FeedForward`` the whole sublayer (layer
+norm, gated block, down projection).  Their ``forward_checkpoint`` returns what
+the backward pass needs beside the result: the quantised activation and its
+scales, one byte per element.  Gradients are straight-through: those of the
+weights that were prepared, dense, for the caller's optimiser, whose updated
+weights make new layers.
 """
 
 import torch
@@ -97,6 +106,29 @@ class SparseFp8Linear:
 
     __call__ = forward
 
+    def forward_checkpoint(self, x):
+        """The forward for training: (y, checkpoint), the checkpoint being the
+        quantised activation [m, k] and its scales [m] in buffers of its own
+        (any number may be kept at a time), the input of ``backward``."""
+        m = x.shape[0]
+        y, a_q, s_a = B.sfp8_sparse_linear_quant(x, self.a_dtype, self.packed, self.w_dtype,
+                                                 self.s_w, self.n, self.k, bias=self.bias,
+                                                 workspace=self.workspace(m))
+        return y, (a_q, s_a)
+
+    def backward(self, dy, checkpoint, need_dx=True, need_dw=True, need_dbias=None):
+        """(dx [m, k], dw [n, k], dbias [n]) bf16 from dy [m, n] bf16 and
+        ``forward_checkpoint``'s checkpoint; None where not asked for (dbias by
+        default: where the layer has a bias)."""
+        a_q, s_a = checkpoint
+        if need_dbias is None:
+            need_dbias = self.bias is not None
+        return B.sfp8_sparse_linear_backward(
+            dy, a_q, self.a_dtype, s_a, self.packed, self.w_dtype, self.s_w, self.n, self.k,
+            need_dx=need_dx, need_dw=need_dw, need_dbias=need_dbias,
+            workspace=_kept(self._ws, ("backward", a_q.shape[0]), B.new_linear_backward_workspace,
+                            a_q.shape[0], self.n, self.k, self.device))
+
     def _act_buffers(self, m):
         """The quantised activation [m, k] and its scales [m] (kept per m)."""
         b = self._act.get(m)
@@ -129,6 +161,128 @@ class SparseFp8Linear:
             x_host, self.a_dtype, self.packed, self.w_dtype, self.s_w, self.n, self.k,
             xs if x_dev is None else x_dev, a_q, s_a, ys if y_dev is None else y_dev, y_host,
             self.workspace(m), bias=self.bias)
+
+
+def _kept(cache, key, new, *sizes):
+    """cache[key], made by new(*sizes) when it is missing."""
+    ws = cache.get(key)
+    if ws is None:
+        ws = cache[key] = new(*sizes)
+    return ws
+
+
+class SparseFp8GatedLinear:
+    """h = act(x W_gate^T + b_gate) * (x W_up^T + b_up) over one compressed weight
+    that holds both, one kernel for the whole block."""
+
+    def __init__(self, w_gate, w_up, bias_gate=None, bias_up=None, act="silu", w_dtype="e4m3",
+                 a_dtype="e4m3"):
+        if w_gate.dim() != 2:
+            raise ValueError("w_gate and w_up must be [hidden, in_features]")
+        if (bias_gate is None) != (bias_up is None):
+            raise ValueError("give both biases or none")
+        self.n, self.k = w_gate.shape
+        self.act, self.w_dtype, self.a_dtype = act, w_dtype, a_dtype
+        self.device = w_gate.device
+        self.packed, self.s_w = B.sfp8_prepare_gated_weight_24(w_gate.contiguous(),
+                                                               w_up.contiguous(), w_dtype)
+        self.bias = None
+        if bias_gate is not None:
+            self.bias = torch.cat((bias_gate, bias_up)).to(torch.bfloat16)
+        self._ws = {}
+
+    def _workspace(self, kind, m):
+        # a changed algorithm table may ask for another size
+        new = {"quant": B.new_gated_quant_workspace, "codes": B.new_gated_workspace,
+               "backward": B.new_gated_backward_workspace}[kind]
+        epoch = 0 if kind == "backward" else B.algo_epoch()
+        return _kept(self._ws, (kind, m, epoch), new, m, self.n, self.k, self.device)
+
+    def forward_checkpoint(self, x, out=None):
+        """(h [m, hidden] bf16, checkpoint) from x [m, k] bf16/f16/f32; the
+        checkpoint (codes and scales of x) is the input of ``backward``.  The
+        layer keeps one workspace per token count, so one call of a layer per
+        token count may be in flight at a time (calls on one stream are
+        ordered); calls captured in graphs that may run at the same time take
+        layers of their own."""
+        h, a_q, s_a = B.sfp8_gated_linear_quant(
+            x, self.a_dtype, self.packed, self.w_dtype, self.s_w, self.n, self.k, act=self.act,
+            bias=self.bias, out=out, workspace=self._workspace("quant", x.shape[0]))
+        return h, (a_q, s_a)
+
+    def forward(self, x, out=None):
+        """h [m, hidden] bf16."""
+        return self.forward_checkpoint(x, out)[0]
+
+    __call__ = forward
+
+    def forward_codes(self, a_q, s_a, out=None):
+        """h from an activation that is already quantised to ``a_dtype`` codes
+        (by ``sfp8_layernorm_quant``, for instance)."""
+        return B.sfp8_gated_linear(a_q, self.a_dtype, s_a, self.packed, self.w_dtype, self.s_w,
+                                   self.n, self.k, act=self.act, bias=self.bias, out=out,
+                                   workspace=self._workspace("codes", a_q.shape[0]))
+
+    def backward(self, dh, checkpoint, need_dx=True, need_dw=True, need_dbias=None):
+        """(dx [m, k], dw [2, hidden, k], dbias [2, hidden]) bf16 from dh [m,
+        hidden] bf16: dw[0], dbias[0] are gate's, dw[1], dbias[1] up's; None
+        where not asked for (dbias by default: where the layer has biases)."""
+        a_q, s_a = checkpoint
+        if need_dbias is None:
+            need_dbias = self.bias is not None
+        dx, dw, db = B.sfp8_gated_linear_backward(
+            dh, a_q, self.a_dtype, s_a, self.packed, self.w_dtype, self.s_w, self.n, self.k,
+            act=self.act, bias=self.bias, need_dx=need_dx, need_dw=need_dw,
+            need_dbias=need_dbias, workspace=self._workspace("backward", a_q.shape[0]))
+        return (dx, None if dw is None else dw.view(2, self.n, self.k),
+                None if db is None else db.view(2, self.n))
+
+
+class SparseFp8FeedForward:
+    """The feed-forward sublayer without its residual addition:
+    y = down(act(gate(norm(x))) * up(norm(x))), the norm going straight to the
+    FP8 codes that the gated block reads."""
+
+    def __init__(self, norm_weight, norm_bias, w_gate, w_up, w_down, act="silu", eps=1e-5,
+                 w_dtype="e4m3", a_dtype="e4m3"):
+        self.norm_weight, self.norm_bias, self.eps = norm_weight, norm_bias, eps
+        self.gated = SparseFp8GatedLinear(w_gate, w_up, act=act, w_dtype=w_dtype, a_dtype=a_dtype)
+        self.down = SparseFp8Linear(w_down, w_dtype=w_dtype, a_dtype=a_dtype)
+        if self.down.k != self.gated.n:
+            raise ValueError("w_down must have one column per hidden unit")
+        self._ws = {}
+
+    def forward_checkpoint(self, x):
+        """(y [m, out] bf16, checkpoint) from x [m, k]; the checkpoint keeps x
+        itself (not a copy), the norm's two statistics per row and the
+        codes and scales of the two quantised activations."""
+        a_q, s_a, mean, rstd = B.sfp8_layernorm_quant(x, self.norm_weight, self.norm_bias,
+                                                      self.eps, self.gated.a_dtype)
+        h = self.gated.forward_codes(a_q, s_a)
+        y, inner = self.down.forward_checkpoint(h)
+        return y, (x, mean, rstd, (a_q, s_a), inner)
+
+    def forward(self, x):
+        """y [m, out] bf16."""
+        return self.forward_checkpoint(x)[0]
+
+    __call__ = forward
+
+    def backward(self, dy, checkpoint):
+        """Gradients from dy [m, out] bf16: a dict with dx (x's dtype), norm_weight
+        and norm_bias (float32), w_gate, w_up and w_down (bf16)."""
+        x, mean, rstd, outer, inner = checkpoint
+        dh, dw_down, _ = self.down.backward(dy, inner)
+        dn, dw, _ = self.gated.backward(dh, outer)
+        # the norm's backward pass takes its gradient in x's type
+        dn = dn if dn.dtype == x.dtype else dn.to(x.dtype)
+        rows, cols = x.shape
+        dx, d_weight, d_bias = B.sfp8_layernorm_backward(
+            dn, x, self.norm_weight, mean, rstd,
+            workspace=_kept(self._ws, rows, B.new_layernorm_backward_workspace, rows, cols,
+                            x.device))
+        return dict(dx=dx, norm_weight=d_weight, norm_bias=d_bias, w_gate=dw[0], w_up=dw[1],
+                    w_down=dw_down)
 
 
 class HostPipeline:
