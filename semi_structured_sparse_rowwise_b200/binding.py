@@ -897,16 +897,16 @@ def _norm_forward(x, weight, bias, eps, out, q, q_dtype, scales, mean, rstd):
 
 def _row_vectors(rows, device, *given):
     """float32 [rows] outputs: the given ones (name, tensor) checked, the
-    others views of one new buffer."""
-    new = [t for _, t in given if t is None]
-    if new:
-        new = list(torch.empty((len(new), rows), dtype=torch.float32, device=device).unbind())
+    others new."""
     out = []
+    new = None
     for what, t in given:
-        if t is None:
-            t = new.pop()
-        else:
+        if t is not None:
             _tensor(t, what, (rows,), torch.float32, device)
+        elif new is None:
+            t = new = torch.empty((rows,), dtype=torch.float32, device=device)
+        else:
+            t = torch.empty_like(new)     # the cheaper call
         out.append(t)
     return out
 

@@ -339,11 +339,11 @@ constexpr int kNormMaxSlots = 8;
 
 
 
-// Ring of row buffers of a row group: slot i % slots holds the group's i-th
-// row (`parts` rows of `bytes` each, from as many tensors).  One thread fills
-// it; the waits are bounded, and after one has run out (the status word says
-// so) the others give up at once and the group runs through on whatever the
-// buffers hold.
+// Ring of row buffers of a row group: its rows go through the slots in turn
+// (`PARTS` rows of `bytes` each, from as many tensors), the group's position
+// kept as a slot and that slot's phase.  One thread fills; the waits are
+// bounded, and after one has run out (the status word says so) the others give
+// up at once and the group runs through on whatever the buffers hold.
 template <int PARTS>
 struct NormRing {
   uint8_t* base;
@@ -351,28 +351,35 @@ struct NormRing {
   volatile int* abort;
   uint32_t bytes;     // of one row, a multiple of 16
   int slots;
-  __device__ uint8_t* slot(int i) const {
-    return base + static_cast<size_t>(i % slots) * PARTS * bytes;
+  int at = 0;         // the current row's slot
+  uint32_t phase = 0; // and its barrier's phase
+  __device__ uint8_t* buffer(int slot) const {
+    return base + static_cast<size_t>(slot) * PARTS * bytes;
   }
-  // The group's i-th row, from a (and b).  Every thread must have finished
-  // with the slot's previous row.
-  __device__ void fill(int i, const void* a, const void* b) const {
-    const uint32_t bar = smem_u32(&full[i % slots]);
+  // A row from a (and b) into `slot`, whose previous row every thread has
+  // finished with.
+  __device__ void fill(int slot, const void* a, const void* b) const {
+    const uint32_t bar = smem_u32(&full[slot]);
     const uint64_t pol = l2_policy_evict_first();
-    uint8_t* dst = slot(i);
+    uint8_t* dst = buffer(slot);
     mbar_arrive_expect_tx(bar, PARTS * bytes);
     bulk_load(smem_u32(dst), a, bytes, bar, pol);
     if (PARTS == 2) bulk_load(smem_u32(dst + bytes), b, bytes, bar, pol);
   }
-  __device__ void wait(int i) const {
-    mbar_wait(smem_u32(&full[i % slots]), static_cast<uint32_t>((i / slots) & 1), abort);
+  __device__ void wait() const { mbar_wait(smem_u32(&full[at]), phase, abort); }
+  __device__ int before() const { return at == 0 ? slots - 1 : at - 1; }
+  __device__ void advance() {
+    if (++at == slots) {
+      at = 0;
+      phase ^= 1u;
+    }
   }
   // One thread, after the group's `rows` rows: where waits were given up, lets
   // the copies still in flight land (again with a limit) before the block
   // goes on to reuse or leave its shared memory.
-  __device__ void drain(int rows) const {
+  __device__ void drain(long long rows) const {
     if (!*abort) return;
-    for (int i = rows > slots ? rows - slots : 0; i < rows; ++i) {
+    for (long long i = rows > slots ? rows - slots : 0; i < rows; ++i) {
       volatile int no_abort = 0;
       mbar_wait(smem_u32(&full[i % slots]), static_cast<uint32_t>((i / slots) & 1), &no_abort);
     }
@@ -460,8 +467,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   float* w_sm = reinterpret_cast<float*>(norm_smem);
   float* b_sm = w_sm + p.cols;
   const uint32_t bytes = static_cast<uint32_t>(p.cols * sizeof(T));
-  const NormRing<1> ring{norm_smem + 8ll * p.cols + static_cast<size_t>(group) * slots * bytes,
-                         full[group], &abort_flag, bytes, slots};
+  NormRing<1> ring{norm_smem + 8ll * p.cols + static_cast<size_t>(group) * slots * bytes,
+                   full[group], &abort_flag, bytes, slots};
   if (threadIdx.x == 0) {
     for (int g = 0; g < kGroups; ++g)
       for (int s = 0; s < slots; ++s) mbar_init(smem_u32(&full[g][s]), 1);
@@ -482,10 +489,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   params_to_shared<T, VEC>(p.bias, p.params_f32, 0.0f, p.cols, b_sm);
   __syncthreads();
   const float inv = 1.0f / static_cast<float>(p.cols);
-  int it = 0;      // rows of the group so far
-  for (long long row = first; row < p.rows; row += stride, ++it) {
-    ring.wait(it);
-    const T* xr = reinterpret_cast<const T*>(ring.slot(it));
+  for (long long row = first; row < p.rows; row += stride, ring.advance()) {
+    ring.wait();
+    const T* xr = reinterpret_cast<const T*>(ring.buffer(ring.at));
     float2 v[N][VEC / 2];
     float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
@@ -500,7 +506,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float mean = group_reduce<TPR, false>(acc.x + acc.y, red[group][0], group) * inv;
     // past the barrier every thread of the group has its part in registers
     if (t == 0 && row + slots * stride < p.rows)
-      ring.fill(it + slots, x + (row + slots * stride) * p.ld_x, nullptr);
+      ring.fill(ring.at, x + (row + slots * stride) * p.ld_x, nullptr);
     acc = make_float2(0.0f, 0.0f);
     const float2 shift = pair_of(-mean);
 #pragma unroll
@@ -572,7 +578,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       else codes(std::integral_constant<int, SFP8_E4M3>{});
     }
   }
-  if (t == 0) ring.drain(it);
+  if (t == 0 && first < p.rows) ring.drain((p.rows - first + stride - 1) / stride);
 }
 
 // ------------------------------------------------------------------ backward
@@ -723,8 +729,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   float* w_sm = reinterpret_cast<float*>(norm_smem);
   const uint32_t bytes = static_cast<uint32_t>(p.cols * sizeof(T));
   uint8_t* rings = norm_smem + 4ll * p.cols;
-  const NormRing<2> ring{rings + static_cast<size_t>(group) * slots * 2 * bytes, full[group],
-                         &abort_flag, bytes, slots};
+  NormRing<2> ring{rings + static_cast<size_t>(group) * slots * 2 * bytes, full[group],
+                   &abort_flag, bytes, slots};
   if (threadIdx.x == 0) {
     for (int g = 0; g < kGroups; ++g)
       for (int s = 0; s < slots; ++s) mbar_init(smem_u32(&full[g][s]), 1);
@@ -750,20 +756,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) dw[i][j] = db[i][j] = make_float2(0.0f, 0.0f);
   const float inv = 1.0f / static_cast<float>(p.cols);
-  int it = 0;      // rows of the group so far
+  int turn = 0;    // alternates by row
   float mean = 0.0f, rstd = 0.0f;
   if (first < p.rows) {
     mean = p.mean[first];
     rstd = p.rstd[first];
   }
-  for (long long row = first; row < p.rows; row += stride, ++it) {
+  for (long long row = first; row < p.rows; row += stride, ring.advance(), turn ^= 1) {
     float mean_n = 0.0f, rstd_n = 0.0f;
     if (row + stride < p.rows) {
       mean_n = p.mean[row + stride];
       rstd_n = p.rstd[row + stride];
     }
-    ring.wait(it);
-    const T* xr = reinterpret_cast<const T*>(ring.slot(it));
+    ring.wait();
+    const T* xr = reinterpret_cast<const T*>(ring.buffer(ring.at));
     const T* dr = xr + p.cols;
     const float2 shift = pair_of(-mean), scale = pair_of(rstd);
     float2 sg = make_float2(0.0f, 0.0f), sgc = make_float2(0.0f, 0.0f);
@@ -792,13 +798,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       sums.x += __shfl_xor_sync(0xffffffffu, sums.x, o);
       sums.y += __shfl_xor_sync(0xffffffffu, sums.y, o);
     }
-    float2(&rd)[TPR / 32] = red[group][it & 1];
+    float2(&rd)[TPR / 32] = red[group][turn];
     if (t % 32 == 0) rd[t / 32] = sums;
     named_barrier_sync(1 + group, TPR);
     // the group has finished with the previous row: refill its slot
-    if (t == 0 && it > 0 && row + (slots - 1) * stride < p.rows) {
+    if (t == 0 && row != first && row + (slots - 1) * stride < p.rows) {
       const long long next = row + (slots - 1) * stride;
-      ring.fill(it - 1 + slots, x + next * p.ld_x, dy + next * p.ld_dy);
+      ring.fill(ring.before(), x + next * p.ld_x, dy + next * p.ld_dy);
     }
     if (p.dx != nullptr) {
       float2 total = rd[0];
@@ -830,7 +836,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     mean = mean_n;
     rstd = rstd_n;
   }
-  if (t == 0) ring.drain(it);
+  if (t == 0 && first < p.rows) ring.drain((p.rows - first + stride - 1) / stride);
   // The rings are done with (every copy has been waited for): the groups add
   // their sums into them in order.
   float* total = reinterpret_cast<float*>(rings);
