@@ -30,8 +30,8 @@
 //                  scalar arithmetic issued 28 million warp instructions for
 //                  8192 rows of 4096 bf16 and took 47 us to codes): hence
 //                  packed fp32 pairs and few, wide threads a row.  8192 x
-//                  4096 bf16: 30 us to codes (3.3 TB/s), 26 us to bf16 (5.2
-//                  TB/s; 28 us with 128 threads a row), 44 us backward (4.5
+//                  4096 bf16: 26 us to codes (3.9 TB/s), 26 us to bf16 (5.2
+//                  TB/s; 28 us with 128 threads a row), 43 us backward (4.7
 //                  TB/s).
 //   long kernels   rows that fit neither read them again from L2.
 // VEC elements make 16 bytes where base, row stride and width allow, else 1.
@@ -451,8 +451,10 @@ __host__ __device__ constexpr int norm_stream_smem(int groups, int params, int c
   return params * cols * 4 + groups * slots * parts * row_bytes;
 }
 
-// N vectors of VEC elements a thread: cols <= TPR * N * VEC, a multiple of VEC.
-template <typename T, int VEC, int TPR, int N, int THREADS, bool Q>
+// N vectors of VEC elements a thread: cols <= TPR * N * VEC, a multiple of VEC;
+// FULL: cols is all of that (a power of two, as most widths are), so that no
+// vector needs a test (8192 x 4096 bf16 to codes: 26 us against 29).
+template <typename T, int VEC, int TPR, int N, int THREADS, bool Q, bool FULL>
 __global__ void __launch_bounds__(THREADS, 1)
     layernorm_stream_kernel(const NormParams p, int slots) {
   extern __shared__ __align__(128) uint8_t norm_smem[];
@@ -497,7 +499,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * TPR + t) * VEC;
-      if (c < p.cols) {
+      if (FULL || c < p.cols) {
         load_pairs<T, VEC>(xr + c, v[i]);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) acc = __fadd2_rn(acc, v[i][j]);
@@ -511,7 +513,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     const float2 shift = pair_of(-mean);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if ((i * TPR + t) * VEC < p.cols) {
+      if (FULL || (i * TPR + t) * VEC < p.cols) {
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
           v[i][j] = __fadd2_rn(v[i][j], shift);
@@ -531,7 +533,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int c = (i * TPR + t) * VEC;
-      if (c < p.cols) {
+      if (FULL || c < p.cols) {
         float2 w[VEC / 2], b[VEC / 2];
         shared_pairs<VEC>(w_sm, i * TPR + t, p.cols, w);
         shared_pairs<VEC>(b_sm, i * TPR + t, p.cols, b);
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const int c = (i * TPR + t) * VEC;
-          if (c < p.cols) {
+          if (FULL || c < p.cols) {
             uint32_t o[VEC / 4];
 #pragma unroll
             for (int j = 0; j < VEC / 4; ++j) {

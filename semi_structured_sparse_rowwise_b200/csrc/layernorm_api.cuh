@@ -88,23 +88,29 @@ sfp8_status launch_norm_stream(DeviceInfo* dev, int slot, Kernel kern, int threa
 // 16-byte vectors.  Few rows (a decode step, fewer than two a SM): as many
 // threads as vectors, so that the chain of one load, three reductions and one
 // store is all a row takes.  Many rows (eight a SM and more): the stream
-// kernel (8192 rows of 4096 bf16 to codes: 30 us, the row kernel with four
+// kernel (8192 rows of 4096 bf16 to codes: 26 us, the row kernel with four
 // vectors a thread 43 us), with as many row groups as its registers allow.
 template <typename T, bool Q>
 sfp8_status launch_norm_vec(DeviceInfo* dev, int kind, const NormParams& p, cudaStream_t st) {
   constexpr int V = InputTraits<T>::kPerVec;
   const int nvec = p.cols / V;
-  const int s0 = kind * 12 + (Q ? 4 : 0);
+  const int s0 = kind * 12 + (Q ? 0 : 8);   // 8 slots to codes, 4 without
   if (nvec <= 32) return launch_norm_rows<T, V, 32, 1, Q>(p, st);
   if (nvec > 64 && nvec <= 1024 && p.rows >= 8ll * dev->num_sms) {
     const int bytes = p.cols * static_cast<int>(sizeof(T));
     auto go = [&](int slot, auto kern, int threads, int per_block) {
       return launch_norm_stream(dev, s0 + slot, kern, threads, per_block, p, 2, 1, bytes, st);
     };
-    if (nvec <= 128) return go(0, layernorm_stream_kernel<T, V, 64, 2, 960, Q>, 960, 15);
-    if (nvec <= 256) return go(1, layernorm_stream_kernel<T, V, 64, 4, 768, Q>, 768, 12);
-    if (nvec <= 512) return go(2, layernorm_stream_kernel<T, V, 64, 8, 512, Q>, 512, 8);
-    return go(3, layernorm_stream_kernel<T, V, 128, 8, 512, Q>, 512, 4);
+    if constexpr (Q) {
+      if (nvec == 128) return go(4, layernorm_stream_kernel<T, V, 64, 2, 960, Q, true>, 960, 15);
+      if (nvec == 256) return go(5, layernorm_stream_kernel<T, V, 64, 4, 768, Q, true>, 768, 12);
+      if (nvec == 512) return go(6, layernorm_stream_kernel<T, V, 64, 8, 512, Q, true>, 512, 8);
+      if (nvec == 1024) return go(7, layernorm_stream_kernel<T, V, 128, 8, 512, Q, true>, 512, 4);
+    }
+    if (nvec <= 128) return go(0, layernorm_stream_kernel<T, V, 64, 2, 960, Q, false>, 960, 15);
+    if (nvec <= 256) return go(1, layernorm_stream_kernel<T, V, 64, 4, 768, Q, false>, 768, 12);
+    if (nvec <= 512) return go(2, layernorm_stream_kernel<T, V, 64, 8, 512, Q, false>, 512, 8);
+    return go(3, layernorm_stream_kernel<T, V, 128, 8, 512, Q, false>, 512, 4);
   }
   if (p.rows < 2ll * dev->num_sms) {
     if (nvec <= 128) return launch_norm_rows<T, V, 128, 1, Q>(p, st);
