@@ -300,6 +300,7 @@ sfp8_status launch_linear_grads(DeviceInfo* dev, const BackwardPlan& bp, const B
       pr.band = 8;   // about as many row tiles as column tiles in flight at a time
       pr.pair_rows = i == 0 ? 0 : static_cast<int>(pair_rows);
       pr.a_mn = i;
+      pr.by_sector = aligned(pr.d, 32);
       pr.idesc = make_idesc_bf16(i == 1, true, kGgTileM, static_cast<uint32_t>(g.bn));
       if (pl.splits > 1) {
         jp.prob[at] = pr;
@@ -365,18 +366,30 @@ sfp8_status validate_backward(const BackwardCall& c, const void* dy, int64_t n, 
 }
 
 // The work split of the gated block's gradient epilogue: always the CTA-pair
-// kernel (no split-K).  The token tile is the widest that leaves a tile for
-// every pair.
+// kernel (no split-K).  Two weight tiles a CTA where the linear's rule takes
+// them; else the token tile with the fewest rounds of tiles times their width
+// (plus 32 tokens' worth of a tile's fixed cost).
 LinearChoice gated_grad_choice(int64_t m, int64_t rows, int64_t k, int num_sms) {
-  if (m >= kPairMinTokens) return default_choice(m, rows, k, num_sms);
+  if (m >= kPairMinTokens) {
+    const LinearChoice d = default_choice(m, rows, k, num_sms);
+    if (d.wt == 2) return d;
+  }
   LinearChoice c{};
   c.pair = 1;
   c.whole = 1;
   c.wt = 1;
   c.ks = (k / kStepK) % 2 == 0 ? 2 : 1;
-  c.bn = pair_bn_for(m);
   const int64_t groups = ((rows + kTileN - 1) / kTileN + 1) / 2;
-  while (c.bn > 32 && groups * ((m + c.bn - 1) / c.bn) < num_sms / 2) c.bn -= 32;
+  const int64_t pairs = num_sms / 2 > 0 ? num_sms / 2 : 1;
+  int64_t best = 0;
+  for (int bn = pair_bn_for(m); bn >= 32; bn -= 32) {
+    const int64_t rounds = (groups * ((m + bn - 1) / bn) + pairs - 1) / pairs;
+    const int64_t cost = rounds * (bn + 32);
+    if (c.bn == 0 || cost < best) {
+      best = cost;
+      c.bn = bn;
+    }
+  }
   return c;
 }
 

@@ -86,6 +86,7 @@ struct GgProblem {
   int band;               // row tiles per band of the tile order
   int pair_rows;          // != 0: D's row r is stored at row (r & 1) * pair_rows + r / 2
   int a_mn;               // A is MN-major
+  int by_sector;          // D is 32-byte aligned
   uint32_t idesc;
 };
 
@@ -117,6 +118,13 @@ __device__ __forceinline__ void mma_bf16_pair_w(uint32_t d_tmem, uint64_t a_desc
       "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+
+// 32 bytes at a 32-byte aligned address: a whole sector in one store.
+__device__ __forceinline__ void store_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
 }
 
 // 2-D form of tma_load_3d_pair.
@@ -400,9 +408,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
             float* dst = pr.partial +
                          (static_cast<long long>(sp) * pr.rows + r) * pr.cols + col;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<uint4*>(dst + 4 * j) =
-                  make_uint4(v[h][4 * j], v[h][4 * j + 1], v[h][4 * j + 2], v[h][4 * j + 3]);
+            for (int j = 0; j < 2; ++j) {
+              uint32_t w[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) w[i] = v[h][8 * j + i];
+              store_sector(dst + 8 * j, w);
+            }
           } else {
             uint32_t w[8];
 #pragma unroll
@@ -412,8 +423,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
               w[j] = *reinterpret_cast<const uint32_t*>(&b2);
             }
             __nv_bfloat16* dst = pr.d + out_row * pr.cols + col;
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-            *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            if (pr.by_sector) {
+              store_sector(dst, w);
+            } else {
+              *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4*>(dst + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         }
       }
