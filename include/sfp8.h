@@ -486,7 +486,8 @@ int sfp8_sparse_linear_quant_fusable(int64_t m, int64_t n, int64_t k);
  *  n       hidden units (0 <= n < 2^30); packed and s_w hold 2n rows.
  *  act     SFP8_ACT_SILU or SFP8_ACT_GELU.
  *  bias    device, [2n] bf16: gate's n values, then up's; or NULL.
- *  h       device, [m, n] bf16, row stride n.
+ *  h       device, [m, n] bf16, row stride n; an h that shares bytes with an
+ *          input is refused with SFP8_ERR_INVALID_ARG.
  *  Everything else as for sfp8_sparse_linear and sfp8_sparse_linear_quant.
  */
 sfp8_status sfp8_prepare_gated_weight_24(const void* w_gate, const void* w_up,
@@ -544,7 +545,8 @@ sfp8_status sfp8_gated_linear_quant(const void* x, sfp8_dtype x_dtype, int64_t l
  *  workspace  16-byte aligned, >= the matching workspace_bytes(m, n, k);
  *          needs no clearing.  Calls that share one must not overlap.
  *  k % 128 == 0, k > 0.  m == 0 or n == 0: the outputs asked for are zeros.
- * Outputs must not overlap each other, the inputs or the workspace.
+ * Outputs that share bytes with each other, the inputs or the workspace are
+ * refused with SFP8_ERR_INVALID_ARG.
  */
 size_t sfp8_sparse_linear_backward_workspace_bytes(int64_t m, int64_t n, int64_t k);
 sfp8_status sfp8_sparse_linear_backward(const void* dy, int64_t ld_dy, const void* a_q,
@@ -584,7 +586,8 @@ sfp8_status sfp8_gated_linear_backward(const void* dh, int64_t ld_dh, const void
  *          NULL (scales and q_dtype are then not looked at).
  *  mean, rstd  device, [rows] float32 each, or NULL; the backward pass takes
  *          them.
- * Outputs must not overlap x, the parameters or each other.
+ * Outputs that share bytes with x, the parameters or each other are refused
+ * with SFP8_ERR_INVALID_ARG.
  */
 sfp8_status sfp8_layernorm(const void* x, sfp8_dtype x_dtype, int64_t rows, int64_t cols,
                            int64_t ld_x, const void* weight, const void* bias,
@@ -606,6 +609,8 @@ sfp8_status sfp8_layernorm(const void* x, sfp8_dtype x_dtype, int64_t rows, int6
  *  workspace  16-byte aligned, >= sfp8_layernorm_backward_workspace_bytes(rows,
  *          cols); needs no clearing.  Calls that share one must not overlap.
  *  rows == 0: dweight and dbias are zeros.
+ * Outputs that share bytes with each other, the inputs or the workspace are
+ * refused with SFP8_ERR_INVALID_ARG.
  */
 size_t sfp8_layernorm_backward_workspace_bytes(int64_t rows, int64_t cols);
 sfp8_status sfp8_layernorm_backward(const void* dy, int64_t ld_dy, const void* x,

@@ -170,6 +170,12 @@ constexpr int64_t kColSumMinRows = 64;   // rows a run at least
 
 size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
+// The parts' offsets count from the workspace's first 256-byte boundary
+// (stores of partial sums are 32 bytes wide); `total` leaves room for it.
+uint8_t* workspace_base(void* workspace) {
+  return reinterpret_cast<uint8_t*>(up256(reinterpret_cast<uintptr_t>(workspace)));
+}
+
 // sum_runs: rows of column sums that the gated gradient epilogue writes, or 0:
 // as many runs as fill the device.
 BackwardPlan backward_plan(int64_t m, int64_t rows, int64_t k, bool keep_dz, int sum_runs,
@@ -195,7 +201,7 @@ BackwardPlan backward_plan(int64_t m, int64_t rows, int64_t k, bool keep_dz, int
   at = up256(at + static_cast<size_t>(b.runs) * static_cast<size_t>(rows) * sizeof(float));
   b.partial_off = at;
   b.grads = grad_plan(m, rows, k, num_sms);
-  b.total = at + up256(b.grads.p[0].partial_bytes) + up256(b.grads.p[1].partial_bytes);
+  b.total = 256 + at + up256(b.grads.p[0].partial_bytes) + up256(b.grads.p[1].partial_bytes);
   return b;
 }
 
@@ -340,6 +346,22 @@ sfp8_status empty_grads(const BackwardCall& c, cudaStream_t st) {
   return SFP8_OK;
 }
 
+// Whether the gradients share bytes with each other, with what the pass reads
+// or with its workspace: it reads everything more than once, and writes one
+// gradient while others are still to be computed.  Sizes are validated.
+bool grads_alias(const BackwardCall& c, const void* dy, int64_t n, int64_t ld_dy,
+                 const void* workspace, size_t workspace_bytes) {
+  const ByteRange outs[] = {{c.dx, 2 * c.m * c.k}, {c.dw, 2 * c.rows * c.k}, {c.dbias, 2 * c.rows}};
+  const ByteRange ins[] = {
+      {dy, 2 * ((c.m - 1) * ld_dy + n)},
+      {c.a_q, c.m * c.k},
+      {c.s_a, 4 * c.m},
+      {c.packed, static_cast<int64_t>(sfp8_compressed_bytes(c.rows, c.k))},
+      {c.s_w, 4 * c.rows},
+      {workspace, static_cast<int64_t>(workspace_bytes)}};
+  return outputs_alias(outs, 3, ins, 6);
+}
+
 // Checks shared by the backward entry points: dy [m, n] with row stride ld_dy;
 // need_act / need_weight say which operands are read.
 sfp8_status validate_backward(const BackwardCall& c, const void* dy, int64_t n, int64_t ld_dy,
@@ -431,13 +453,14 @@ sfp8_status sfp8_sparse_linear_backward(const void* dy, int64_t ld_dy, const voi
   // TMA reads dy in place where it can; odd widths go through a padded copy
   const bool in_place = aligned(dy, 16) && ld_dy % 8 == 0;
   if (!in_place && n % 8 == 0) return SFP8_ERR_MISALIGNED;
+  if (grads_alias(c, dy, n, ld_dy, workspace, workspace_bytes)) return SFP8_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;
   s = current_device(&dev);
   if (s != SFP8_OK) return s;
   const BackwardPlan bp = backward_plan(m, n, k, n % 8 != 0, 0, dev->num_sms);
   if (workspace == nullptr || workspace_bytes < bp.total) return SFP8_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return SFP8_ERR_MISALIGNED;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = workspace_base(workspace);
   const bool copy = !in_place && (dx != nullptr || dw != nullptr);
   s = launch_prologue(dev, bp, c, true, dy, ld_dy, copy, dbias != nullptr, ws, st);
   if (s != SFP8_OK) return s;
@@ -471,6 +494,7 @@ sfp8_status sfp8_gated_linear_backward(const void* dh, int64_t ld_dh, const void
   if (!aligned(bias, 2)) return SFP8_ERR_MISALIGNED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (empty) return empty_grads(c, st);
+  if (grads_alias(c, dh, n, ld_dh, workspace, workspace_bytes)) return SFP8_ERR_INVALID_ARG;
   DeviceInfo* dev = nullptr;
   s = current_device(&dev);
   if (s != SFP8_OK) return s;
@@ -479,7 +503,7 @@ sfp8_status sfp8_gated_linear_backward(const void* dh, int64_t ld_dh, const void
   if (workspace == nullptr || workspace_bytes < bp.total) return SFP8_ERR_WORKSPACE;
   if (!aligned(workspace, 16)) return SFP8_ERR_MISALIGNED;
   if (dx == nullptr && dw == nullptr && dbias == nullptr) return SFP8_OK;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  uint8_t* ws = workspace_base(workspace);
   s = launch_prologue(dev, bp, c, false, nullptr, 0, false, false, ws, st);
   if (s != SFP8_OK) return s;
   const LinearPlan pl =

@@ -20,7 +20,11 @@
 // fp32 sums:
 //     dx[m, k] = 1 / s_a[m] * sum_r dz'[m, r] W_q[r, k]
 //     dw[r, k] = 1 / s_w[r] * sum_m dz'[m, r] A_q[m, k]
-// Scales are at least 1e-12 / 57344, so dz' and the quotients stay in range.
+// The quantisers' scales are at least 1e-12 / 57344, which keeps dz' and the
+// quotients in range; where both scales are that small (an all-zero row of
+// the activation against an all-zero row of the weight), dz' may lose its
+// last bits, but then the codes it is multiplied with are zeros in both
+// products.
 //
 // Of a chunk's 16 tokens the gate lane finishes tokens 0..7 and the up lane
 // 8..15: each sends its neighbour the eight values that one needs (8 shuffles

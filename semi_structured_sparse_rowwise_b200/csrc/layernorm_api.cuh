@@ -259,6 +259,17 @@ sfp8_status sfp8_layernorm(const void* x, sfp8_dtype x_dtype, int64_t rows, int6
                    aligned(bias, 16);
   if (q != nullptr && (!vec || !aligned(q, 16) || !aligned(scales, 4))) return SFP8_ERR_MISALIGNED;
   if (y == nullptr && q == nullptr && mean == nullptr && rstd == nullptr) return SFP8_OK;
+  {
+    // rows are read while others are written, and long ones more than once
+    const ByteRange outs[] = {{y, rows * cols * es},
+                              {q, rows * cols},
+                              {q != nullptr ? scales : nullptr, 4 * rows},
+                              {mean, 4 * rows},
+                              {rstd, 4 * rows}};
+    const ByteRange ins[] = {{x, ((rows - 1) * ld_x + cols) * es}, {weight, cols * ps},
+                             {bias, cols * ps}};
+    if (outputs_alias(outs, 5, ins, 3)) return SFP8_ERR_INVALID_ARG;
+  }
   DeviceInfo* dev = nullptr;
   const sfp8_status s = current_device(&dev);
   if (s != SFP8_OK) return s;
@@ -324,6 +335,16 @@ sfp8_status sfp8_layernorm_backward(const void* dy, int64_t ld_dy, const void* x
   if (dy == nullptr || x == nullptr || mean == nullptr || rstd == nullptr)
     return SFP8_ERR_INVALID_ARG;
   if (dx == nullptr && !sums) return SFP8_OK;
+  {
+    const ByteRange outs[] = {{dx, rows * cols * es}, {dweight, 4 * cols}, {dbias, 4 * cols}};
+    const ByteRange ins[] = {{x, ((rows - 1) * ld_x + cols) * es},
+                             {dy, ((rows - 1) * ld_dy + cols) * es},
+                             {weight, cols * elem_size(p_dtype)},
+                             {mean, 4 * rows},
+                             {rstd, 4 * rows},
+                             {workspace, static_cast<int64_t>(workspace_bytes)}};
+    if (outputs_alias(outs, 3, ins, 6)) return SFP8_ERR_INVALID_ARG;
+  }
   DeviceInfo* dev = nullptr;
   sfp8_status s = current_device(&dev);
   if (s != SFP8_OK) return s;

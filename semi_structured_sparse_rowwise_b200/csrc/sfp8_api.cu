@@ -706,6 +706,29 @@ bool outputs_overlap_input(const void* x, sfp8_dtype x_dtype, int64_t ld_x, int6
   return hits(a_q, m * k) || hits(s_a, 4 * m) || hits(y, 2 * m * n);
 }
 
+// Whether [a, a + na) and [b, b + nb) share bytes (null: no).
+bool ranges_overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  if (a == nullptr || b == nullptr || na <= 0 || nb <= 0) return false;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + static_cast<uintptr_t>(nb) && y < x + static_cast<uintptr_t>(na);
+}
+
+struct ByteRange {
+  const void* p;
+  int64_t bytes;
+};
+
+// Whether any output shares bytes with an input, or with another output.
+bool outputs_alias(const ByteRange* outs, int n_outs, const ByteRange* ins, int n_ins) {
+  for (int i = 0; i < n_outs; ++i) {
+    for (int j = 0; j < n_ins; ++j)
+      if (ranges_overlap(outs[i].p, outs[i].bytes, ins[j].p, ins[j].bytes)) return true;
+    for (int j = 0; j < i; ++j)
+      if (ranges_overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return true;
+  }
+  return false;
+}
+
 // The activation that the one-call forward reads (for the overlap check).
 struct XSpan {
   const void* x;
@@ -1702,6 +1725,20 @@ static sfp8_status validate_gated(int64_t n, int act) {
   return SFP8_OK;
 }
 
+// Whether h shares bytes with what the GEMM reads while it writes it (sizes
+// validated, rows = 2n).
+static bool gated_output_alias(const void* h, const void* a_q, const float* s_a, int64_t m,
+                               const void* packed, const float* s_w, int64_t rows, int64_t k,
+                               const void* bias) {
+  const ByteRange outs[] = {{h, m * rows}};
+  const ByteRange ins[] = {{a_q, m * k},
+                           {s_a, 4 * m},
+                           {packed, static_cast<int64_t>(sfp8_compressed_bytes(rows, k))},
+                           {s_w, 4 * rows},
+                           {bias, 2 * rows}};
+  return outputs_alias(outs, 1, ins, 5);
+}
+
 sfp8_status sfp8_prepare_gated_weight_24(const void* w_gate, const void* w_up,
                                          sfp8_dtype w_dtype, int64_t n, int64_t k, int64_t ld_w,
                                          sfp8_dtype q_dtype, void* packed, float* s_w,
@@ -1728,6 +1765,7 @@ sfp8_status sfp8_gated_linear(const void* a_q, sfp8_dtype a_dtype, const float* 
   s = validate_linear(a_q, a_dtype, s_a, m, packed, w_dtype, s_w, 2 * n, k, bias, h, &dev, &pl,
                       &empty);
   if (s != SFP8_OK || empty) return s;
+  if (gated_output_alias(h, a_q, s_a, m, packed, s_w, 2 * n, k, bias)) return SFP8_ERR_INVALID_ARG;
   const size_t need = pl.partial_bytes + pl.counter_bytes;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return SFP8_ERR_WORKSPACE;
   if (workspace != nullptr && !aligned(workspace, 16)) return SFP8_ERR_MISALIGNED;
@@ -1752,6 +1790,9 @@ sfp8_status sfp8_gated_linear_quant(const void* x, sfp8_dtype x_dtype, int64_t l
                                     void* stream) {
   const sfp8_status s = validate_gated(n, act);
   if (s != SFP8_OK) return s;
+  if (m > 0 && m < (int64_t(1) << 31) && k > 0 && k < (int64_t(1) << 31) &&
+      gated_output_alias(h, a_q, s_a, m, packed, s_w, 2 * n, k, bias))
+    return SFP8_ERR_INVALID_ARG;
   const GatedCall gc{kEpiGated, act, nullptr, 0, n, nullptr};
   return quant_linear(x, x_dtype, ld_x, a_dtype, a_q, s_a, m, packed, w_dtype, s_w, 2 * n, k,
                       bias, h, workspace, workspace_bytes, stream, kQuantChained, &gc);

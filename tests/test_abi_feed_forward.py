@@ -93,6 +93,13 @@ def test_linear_backward(lib):
         assert call(f, BACK, **{name: None}) == INVALID
     assert call(f, BACK, ld=12) == MISALIGNED          # rows that TMA cannot read
     assert call(f, BACK, dy=ctypes.c_void_p(0x10002)) == MISALIGNED
+    apart = dict(dx=ctypes.c_void_p(0x20000), dw=ctypes.c_void_p(0x30000),
+                 dbias=ctypes.c_void_p(0x40000), ws=ctypes.c_void_p(0x50000))
+    for name in ("dx", "dw", "dbias"):                 # a gradient over an input, or another
+        assert call(f, BACK, **{**apart, name: FAKE}) == INVALID
+        other = "dw" if name == "dx" else "dx"
+        assert call(f, BACK, **{**apart, name: apart[other]}) == INVALID
+        assert call(f, BACK, **{**apart, name: apart["ws"], "ws_bytes": 64}) == INVALID
 
 
 def test_gated_backward(lib):
@@ -120,6 +127,12 @@ def test_layernorm(lib):
     for name in ("x", "y", "weight", "bias", "mean", "rstd", "q", "scales"):
         assert call(f, good, **{name: ODD}) == MISALIGNED
     assert call(f, good, ld=68) == MISALIGNED          # codes need 16-byte rows
+    apart = {n: ctypes.c_void_p(0x20000 + 0x1000 * i)
+             for i, n in enumerate(("y", "q", "scales", "mean", "rstd"))}
+    for name in apart:
+        assert call(f, good, **{**apart, name: FAKE}) == INVALID      # over x
+        other = "q" if name == "y" else "y"
+        assert call(f, good, **{**apart, name: apart[other]}) == INVALID
     assert call(f, good, rows=0) == 0
 
 
@@ -137,6 +150,11 @@ def test_layernorm_backward(lib):
     for name in ("dx", "dw", "db", "weight"):
         assert call(f, good, **{name: ODD}) == MISALIGNED
     assert call(f, good, dx=None, dw=None, db=None) == 0     # nothing asked for
+    apart = dict(dx=ctypes.c_void_p(0x20000), dw=ctypes.c_void_p(0x30000),
+                 db=ctypes.c_void_p(0x40000))
+    for name in apart:
+        assert call(f, good, **{**apart, name: FAKE}) == INVALID
+        assert call(f, good, **{**apart, name: apart["dx" if name == "dw" else "dw"]}) == INVALID
     assert lib.sfp8_layernorm_backward_workspace_bytes(0, 64) == 0
 
 

@@ -183,6 +183,49 @@ def test_repeats_bit_for_bit_and_shares_a_workspace():
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+def test_outputs_and_workspaces_at_any_allowed_alignment():
+    """16-byte aligned gradients and workspaces that are not 32-byte aligned,
+    with a split contraction (few rows of dx, many weight rows)."""
+    m, n, k = 60, 5000, 128
+    a_q, s_a, _, s_w, packed = operands(m, n, k, 14)
+    dy = torch.randn(m, n, device="cuda", generator=gen(9)).to(torch.bfloat16)
+    args = (dy, a_q, "e4m3", s_a, packed, "e4m3", s_w, n, k)
+    want = S.sfp8_sparse_linear_backward(*args, need_dbias=True)
+
+    def off(numel, dtype, by):
+        return torch.zeros(numel + by, dtype=dtype, device="cuda")[by:]
+
+    ws = S.new_linear_backward_workspace(m, n, k, "cuda")
+    got = S.sfp8_sparse_linear_backward(
+        *args, dx=off(m * k, torch.bfloat16, 8).view(m, k),
+        dw=off(n * k, torch.bfloat16, 8).view(n, k), dbias=off(n, torch.bfloat16, 1),
+        workspace=off(ws.numel(), torch.uint8, 16))
+    assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_gated_backward_with_zero_rows():
+    """All-zero rows of the activation and of both weights: their scales are the
+    quantiser's guard, 1e-12 over the format's largest value."""
+    m, n, k = 48, 40, 256
+    rows = sparse_weight(2 * n, k, 3, 0.05)
+    rows[0:6] = 0
+    codes, s_w = quantise_rows(rows, "e4m3")
+    x = torch.randn(m, k, device="cuda", generator=gen(1)).to(torch.bfloat16)
+    x[::5] = 0
+    a_q, s_a = quantise_rows(x, "e4m3")
+    dh = torch.randn(m, n, device="cuda", generator=gen(9)).to(torch.bfloat16)
+    b = (torch.randn(2 * n, device="cuda", generator=gen(3))).to(torch.bfloat16)
+    got = S.sfp8_gated_linear_backward(dh, a_q, "e4m3", s_a, S.sfp8_compress_24(codes, "e4m3"),
+                                       "e4m3", s_w, n, k, bias=b, need_dbias=True)
+    a, w = decode(a_q, "e4m3"), decode(codes, "e4m3")
+    gate, up, _, _ = gated_reference(a, s_a, w, s_w, b, "silu")
+    dz, err = gated_grad_reference(dh, gate, up, 1e-3 * linear_parts(a, s_a, w, s_w)[1], "silu")
+    refs = backward_reference(dz, err, a, s_a, w, s_w)
+    order = torch.cat((torch.arange(0, 2 * n, 2), torch.arange(1, 2 * n, 2))).cuda()
+    within(got, [refs[0], tuple(t[order] for t in refs[1]), tuple(t[order] for t in refs[2])])
+    assert bool((got[0] != 0).any(1).all())       # a zero row of x has an input gradient too
+
+
 def test_captured_on_a_side_stream():
     m, n, k = 320, 300, 512
     a_q, s_a, _, s_w, packed = operands(m, 2 * n, k, 13)

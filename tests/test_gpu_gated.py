@@ -163,6 +163,9 @@ def test_wrapper_refusals():
         big = torch.zeros(4 * 128, device="cuda", dtype=torch.bfloat16)
         S.sfp8_gated_linear_quant(big.view(4, 128), "e4m3", packed, "e4m3", s_w, 8, 128,
                                   out=big[:32].view(4, 8))
+    with pytest.raises(S.Sfp8Error):     # h would overwrite the codes
+        q = torch.zeros(4 * 128, device="cuda", dtype=torch.uint8)
+        call(a_q=q.view(4, 128), out=q[:64].view(torch.bfloat16).view(4, 8))
     with pytest.raises(ValueError):
         S.sfp8_prepare_gated_weight_24(x, x[:, :64])
     assert B.ACTIVATION == {"silu": 0, "gelu": 1}

@@ -278,7 +278,8 @@ def test_refusals():
                 lambda: S.sfp8_layernorm_backward(x, x, w, mean[:2], mean)):
         with pytest.raises(ValueError):
             bad()
-    for bad in (lambda: S.sfp8_layernorm(x, w, b, -1.0),
+    for bad in (lambda: S.sfp8_layernorm(x, w, b, out=x),      # over its input
+                lambda: S.sfp8_layernorm(x, w, b, -1.0),
                 lambda: S.sfp8_layernorm(x, w, b, float("nan")),
                 lambda: S.sfp8_layernorm(x, w, b, float("inf")),
                 lambda: S.sfp8_layernorm_quant(x[:, :60], w[:60], b[:60]),
