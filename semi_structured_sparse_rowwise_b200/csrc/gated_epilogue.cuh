@@ -48,31 +48,83 @@ enum Epilogue : int {
 // act(g) and act'(g).  Both activations are g * p(g) with a logistic p:
 // SiLU's p = sigma(g); GELU in its tanh form is g * sigma(2 q) with
 // q = sqrt(2/pi) (g + 0.044715 g^3), since (1 + tanh q) / 2 = sigma(2 q) --
-// which also keeps full relative accuracy where 1 + tanh q cancels.  The
-// fast exponential and division err by a few 2^-22, far below the bf16
-// rounding of the result.
-__device__ __forceinline__ float logistic(float x) {
-  // x -> -inf: exp overflows to inf and the quotient is 0
-  return __fdividef(1.0f, 1.0f + __expf(-x));
-}
-
+// which also keeps full relative accuracy where 1 + tanh q cancels.  Then
+//     act = g p,   act' = p + act (1 - p) x'     (p = sigma(x))
+// The approximate exponential and reciprocal err by a few 2^-22, far below
+// the bf16 rounding of the result; they flush what is below 2^-126 to zero,
+// and an exponential that overflows makes p zero.
+//
+// The epilogue's warps share the SM's issue slots with the warps that feed the
+// tensor core, so it counts instructions: hence the raw forms of both, the
+// branch on the activation outside the loops, and 16-token chunks that are
+// known to lie inside the tensors as a whole.
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kGeluC = 0.7978845608028654f;   // sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ float act_value(float g, int act) {
-  const float x = act == SFP8_ACT_SILU ? g : 2.0f * kGeluC * fmaf(kGeluA * g * g, g, g);
-  return g * logistic(x);
+// sigma(x) from -x log2(e).
+__device__ __forceinline__ float logistic_exp2(float t) {
+  float e, p;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.0f + e));
+  return p;
 }
 
-__device__ __forceinline__ void act_value_grad(float g, int act, float& f, float& df) {
-  const float g2 = g * g;
-  const float x = act == SFP8_ACT_SILU ? g : 2.0f * kGeluC * fmaf(kGeluA * g2, g, g);
-  const float dx = act == SFP8_ACT_SILU ? 1.0f : 2.0f * kGeluC * fmaf(3.0f * kGeluA, g2, 1.0f);
-  const float p = logistic(x);
+template <int ACT>
+__device__ __forceinline__ float act_logistic(float g) {
+  if constexpr (ACT == SFP8_ACT_SILU) return logistic_exp2(-kLog2e * g);
+  return logistic_exp2(-2.0f * kLog2e * kGeluC * fmaf(kGeluA * g * g, g, g));
+}
+
+template <int ACT>
+__device__ __forceinline__ void act_value_grad(float g, float& f, float& df) {
+  const float p = act_logistic<ACT>(g);
   f = g * p;
-  const float d = p * (1.0f - p);
-  // where p has saturated the second term is zero (dx may have overflowed)
-  df = d > 0.0f ? fmaf(g * d, dx, p) : p;
+  const float t = f * (1.0f - p);
+  if constexpr (ACT == SFP8_ACT_SILU) {
+    df = p + t;
+  } else {
+    // where p has saturated t is zero, and x' may have overflowed
+    const float dx = 2.0f * kGeluC * fmaf(3.0f * kGeluA * g, g, 1.0f);
+    df = t != 0.0f ? fmaf(t, dx, p) : p;
+  }
+}
+
+// h of eight gate and up values.
+__device__ __forceinline__ void gated_values(const float (&g)[8], const float (&u)[8], int act,
+                                             float (&h)[8]) {
+  if (act == SFP8_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = g[j] * act_logistic<SFP8_ACT_SILU>(g[j]) * u[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = g[j] * act_logistic<SFP8_ACT_GELU>(g[j]) * u[j];
+  }
+}
+
+// act and act' of eight gate values.
+__device__ __forceinline__ void gated_slopes(const float (&g)[8], int act, float (&f)[8],
+                                             float (&df)[8]) {
+  if (act == SFP8_ACT_SILU) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) act_value_grad<SFP8_ACT_SILU>(g[j], f[j], df[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) act_value_grad<SFP8_ACT_GELU>(g[j], f[j], df[j]);
+  }
+}
+
+// z of a chunk: acc * (sa * sw) + bias, two tokens at a time.
+__device__ __forceinline__ void gated_preactivation(const float (&acc)[16], const float (&sa)[16],
+                                                    float sw, float bias, float (&z)[16]) {
+  const float2 sw2 = make_float2(sw, sw), b2 = make_float2(bias, bias);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float2 t = __ffma2_rn(make_float2(acc[2 * j], acc[2 * j + 1]),
+                                __fmul2_rn(make_float2(sa[2 * j], sa[2 * j + 1]), sw2), b2);
+    z[2 * j] = t.x;
+    z[2 * j + 1] = t.y;
+  }
 }
 
 // Index of row r's bias: the caller's vector holds the n gate values, then

@@ -865,6 +865,7 @@ sfp8_status launch_pair_cfg(DeviceInfo* dev, const LinearPlan& pl, const void* a
     prm.ld_dh = gc->ld_dh;
     prm.ld_out = gc->ld_out;
     prm.col_sums = gc->col_sums;
+    prm.sa_by_16 = aligned(s_a, 16);
   }
   return launch_dependent(kern, dim3(2 * pairs), dim3(Cfg::kThreads), pl.smem_bytes, st, tw2,
                           tw, ta, prm);

@@ -210,18 +210,18 @@ __device__ __forceinline__ void store_chunk(const LinearParams& p, const float (
                                             const float (&sa)[16], int n, int m0, float sw,
                                             float bias) {
   if constexpr (EPI == kEpiGated) {
-    float z[16], g[8], u[8];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) z[j] = fmaf(acc[j], sa[j] * sw, bias);
+    float z[16], g[8], u[8], h[8];
+    gated_preactivation(acc, sa, sw, bias, z);
     gated_pair_up(z, n & 1, g, u);
     if (n >= p.n) return;
+    gated_values(g, u, p.act, h);
     const int first = m0 + (n & 1) * 8;
     const int width = p.n >> 1;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       if (first + j < p.m)
         p.y[static_cast<long long>(first + j) * width + (n >> 1)] =
-            __float2bfloat16_rn(act_value(g[j], p.act) * u[j]);
+            __float2bfloat16_rn(h[j]);
     return;
   }
   if (n >= p.n) return;
@@ -685,15 +685,15 @@ __global__ void __launch_bounds__(linear_threads(FQ), 1)
           // (gated: [BN tokens][64 hidden units])
           __nv_bfloat16* stg = reinterpret_cast<__nv_bfloat16*>(ra_base);
           if constexpr (EPI == kEpiGated) {
-            float z[16], g[8], u2[8];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) z[j] = fmaf(v[j], sa[j] * sw, bv);
+            float z[16], g[8], u2[8], h[8];
+            gated_preactivation(v, sa, sw, bv, z);
             gated_pair_up(z, n_local & 1, g, u2);
+            gated_values(g, u2, p.act, h);
             const int first = c * 16 + (n_local & 1) * 8;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               stg[(first + j) * (kTileN / 2) + n_local / 2] =
-                  __float2bfloat16_rn(act_value(g[j], p.act) * u2[j]);
+                  __float2bfloat16_rn(h[j]);
           } else {
 #pragma unroll
             for (int j = 0; j < 16; ++j)

@@ -118,6 +118,7 @@ struct PairParams {
   long long ld_dh;
   long long ld_out;         // row stride of y: h's n / 2, dz's padded width
   float* col_sums;          // [m_tiles * parts][n] sums of dz over tokens, or null
+  int sa_by_16;             // s_a is 16-byte aligned
 };
 
 // Tile t -> (weight group g, token tile mt).  Tiles run in bands of p.band
@@ -140,6 +141,44 @@ __device__ __forceinline__ void pair_tile_coords(const PairParams& p, int t, int
 __device__ __forceinline__ void load_sa_pair(const PairParams& p, int m0, float (&sa)[16]) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) sa[j] = (m0 + j < p.m) ? __ldg(p.s_a + m0 + j) : 0.0f;
+}
+
+// The 16 scales of a chunk that lies inside the tensor, s_a 16-byte aligned (a
+// chunk starts at a multiple of 16 tokens).
+__device__ __forceinline__ void load_sa_full(const PairParams& p, int m0, float (&sa)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 t = __ldg(reinterpret_cast<const float4*>(p.s_a + m0) + j);
+    sa[4 * j] = t.x;
+    sa[4 * j + 1] = t.y;
+    sa[4 * j + 2] = t.z;
+    sa[4 * j + 3] = t.w;
+  }
+}
+
+// Stores of the gated epilogues: this lane's eight tokens of a chunk, from
+// token `first` on; FULL: none of them is past the last.
+template <bool FULL>
+__device__ __forceinline__ void store_gated(const PairParams& p, int first, int n,
+                                            const float (&h)[8]) {
+  __nv_bfloat16* dst = p.y + static_cast<long long>(first) * p.ld_out + (n >> 1);
+#pragma unroll
+  for (int j = 0; j < 8; ++j, dst += p.ld_out)
+    if (FULL || first + j < p.m) *dst = __float2bfloat16_rn(h[j]);
+}
+
+// dz of gate and up, neighbours in a row, with the scales in.
+template <bool FULL>
+__device__ __forceinline__ void store_gated_grad(const PairParams& p, int first, int n,
+                                                 const float (&d)[8], const float (&u)[8],
+                                                 const float (&f)[8], const float (&df)[8],
+                                                 float sw_gate, float sw_up) {
+  __nv_bfloat16* dst = p.y + static_cast<long long>(first) * p.ld_out + (n & ~1);
+#pragma unroll
+  for (int j = 0; j < 8; ++j, dst += p.ld_out)
+    if (FULL || first + j < p.m)
+      *reinterpret_cast<__nv_bfloat162*>(dst) =
+          __floats2bfloat162_rn(d[j] * u[j] * (df[j] * sw_gate), d[j] * (f[j] * sw_up));
 }
 
 template <int KS, int WT, int EPI = kEpiLinear>
@@ -385,10 +424,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT, EPI>
       const unsigned short* dh_col = nullptr;
       unsigned short dh_next[8];
       auto load_dh = [&](int c) {
+        const int m0 = m_tile0 + c * 16;
+        if (m0 + 16 <= p.m) {
+          const unsigned short* src = dh_col + static_cast<long long>(m0 + odd8) * p.ld_dh;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int m = m_tile0 + c * 16 + odd8 + j;
-          dh_next[j] = __ldg(dh_col + static_cast<long long>(m < p.m ? m : p.m - 1) * p.ld_dh);
+          for (int j = 0; j < 8; ++j, src += p.ld_dh) dh_next[j] = __ldg(src);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int m = m0 + odd8 + j;
+            dh_next[j] = __ldg(dh_col + static_cast<long long>(m < p.m ? m : p.m - 1) * p.ld_dh);
+          }
         }
       };
       if constexpr (EPI == kEpiGatedGrad) {
@@ -410,7 +456,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT, EPI>
         uint32_t r[16];
         tmem_ld_32x32b_x16(t_row + c * 16, r);
         float sa[16];
-        load_sa_pair(p, m_tile0 + c * 16, sa);
+        const bool full = m_tile0 + c * 16 + 16 <= p.m;   // every token of the chunk exists
+        if (EPI != kEpiLinear && full && p.sa_by_16) load_sa_full(p, m_tile0 + c * 16, sa);
+        else load_sa_pair(p, m_tile0 + c * 16, sa);
         if constexpr (EPI == kEpiLinear) {
           tmem_ld_wait();
           if (n < p.n) {
@@ -432,27 +480,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairCfg<KS, WT, EPI>
             if (c + kParts < chunks) load_dh(c + kParts);
           }
           tmem_ld_wait();
-          float z[16], g[8], u[8];
+          float v[16], z[16], g[8], u[8];
 #pragma unroll
-          for (int j = 0; j < 16; ++j) z[j] = fmaf(__uint_as_float(r[j]), sa[j] * sw, bv);
+          for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+          gated_preactivation(v, sa, sw, bv, z);
           gated_pair_up(z, n & 1, g, u);
-          if (n < p.n) {
+          if constexpr (EPI == kEpiGated) {
+            float h[8];
+            gated_values(g, u, p.act, h);
+            if (n < p.n) {
+              if (full) store_gated<true>(p, first, n, h);
+              else store_gated<false>(p, first, n, h);
+            }
+          } else {
+            float f[8], df[8], d[8];
+            gated_slopes(g, p.act, f, df);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (first + j >= p.m) continue;
-              __nv_bfloat16* row = p.y + static_cast<long long>(first + j) * p.ld_out;
-              if constexpr (EPI == kEpiGated) {
-                row[n >> 1] = __float2bfloat16_rn(act_value(g[j], p.act) * u[j]);
-              } else {
-                float f, df;
-                act_value_grad(g[j], p.act, f, df);
-                // gate's and up's gradient with the scales in, neighbours in dz
-                const float d_gate = dh[j] * u[j] * df, d_up = dh[j] * f;
-                sum_gate += d_gate;
-                sum_up += d_up;
-                const float s = (n & 1) ? sa[j + 8] : sa[j];
-                *reinterpret_cast<__nv_bfloat162*>(row + (n & ~1)) =
-                    __floats2bfloat162_rn(d_gate * (s * sw_gate), d_up * (s * sw_up));
+            for (int j = 0; j < 8; ++j) d[j] = dh[j] * ((n & 1) ? sa[j + 8] : sa[j]);
+            if (n < p.n) {
+              if (full) store_gated_grad<true>(p, first, n, d, u, f, df, sw_gate, sw_up);
+              else store_gated_grad<false>(p, first, n, d, u, f, df, sw_gate, sw_up);
+            }
+            if (p.col_sums != nullptr) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                if (!full && first + j >= p.m) continue;
+                sum_gate = fmaf(dh[j] * u[j], df[j], sum_gate);
+                sum_up = fmaf(dh[j], f[j], sum_up);
               }
             }
           }
