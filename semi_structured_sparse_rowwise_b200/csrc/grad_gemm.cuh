@@ -564,9 +564,9 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
 constexpr int kExpandRows = 64;
 
 // What[r, k] = bf16(dec(W_q[r, k]) * s_w[r]), dense, half a 128 x 128 tile of
-// the packed weight at a time: every thread takes 4 pieces of 8 k (4 kept
-// codes, 2 index nibbles), neighbouring threads neighbouring words of the tile and
-// neighbouring 16-byte vectors of a row.  With s_w the one rounding (half a
+// the packed weight at a time: every thread takes pieces of 16 k (8 kept codes,
+// 4 index nibbles), neighbouring threads neighbouring words of the tile and
+// neighbouring 32-byte sectors of a row.  With s_w the one rounding (half a
 // bf16 step) is that of the operand; without it (null: the scales are in dz)
 // the codes are exact in bf16.
 __device__ __forceinline__ void expand_weight(const PrologueParams& p, int block) {
@@ -578,18 +578,19 @@ __device__ __forceinline__ void expand_weight(const PrologueParams& p, int block
     const long long tile0 = half / 2 * 128ll;
     __nv_bfloat16* out = p.what + tile0 * p.k + kt * 128ll;
 #pragma unroll
-    for (int i = 0; i < kExpandRows / 16; ++i) {
+    for (int i = 0; i < kExpandRows / 32; ++i) {
       const int item = i * 256 + threadIdx.x;
-      const int r = half % 2 * kExpandRows + item / 16, j = item % 16;
+      const int r = half % 2 * kExpandRows + item / 8, j = item % 8;   // piece of 16 k
       if (tile0 + r >= p.rows) continue;
-      const uint32_t vals = __ldg(reinterpret_cast<const uint32_t*>(
-          tile + 64 * r + (((j / 4) ^ (r >> 1 & 3)) * 16) + (j % 4) * 4));
-      const uint32_t meta = __ldg(tile + 8192 + 16 * r + j);
+      const uint2 vals = __ldg(reinterpret_cast<const uint2*>(
+          tile + 64 * r + (((j / 2) ^ (r >> 1 & 3)) * 16) + (j % 2) * 8));
+      const uint32_t meta = __ldg(reinterpret_cast<const uint16_t*>(tile + 8192 + 16 * r + 2 * j));
       const float s = p.s_w != nullptr ? __ldg(p.s_w + tile0 + r) : 1.0f;
-      uint32_t w[4];
+      uint32_t w[8];
 #pragma unroll
-      for (int g = 0; g < 2; ++g) {
-        const float2 f = fp8_pair_to_float((vals >> (16 * g)) & 0xFFFFu, p.w_fmt);
+      for (int g = 0; g < 4; ++g) {
+        const float2 f = fp8_pair_to_float(((g < 2 ? vals.x : vals.y) >> (16 * (g % 2))) & 0xFFFFu,
+                                           p.w_fmt);
         const uint32_t bits = bf16_pair(f.x * s, f.y * s);
         const uint32_t nib = (meta >> (4 * g)) & 0xFu;
         // the group's four bf16 as one 64-bit word
@@ -599,7 +600,7 @@ __device__ __forceinline__ void expand_weight(const PrologueParams& p, int block
         w[2 * g] = static_cast<uint32_t>(word);
         w[2 * g + 1] = static_cast<uint32_t>(word >> 32);
       }
-      *reinterpret_cast<uint4*>(out + r * p.k + 8 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+      store_sector(out + r * p.k + 16 * j, w);
     }
   }
 }
@@ -614,21 +615,20 @@ __device__ __forceinline__ void expand_rows(const PrologueParams& p, int block) 
     const long long row0 = static_cast<long long>(mt) * kExpandRows;
     const long long at = row0 * p.k + (u - mt * ktiles) * 128ll;
 #pragma unroll
-    for (int i = 0; i < kExpandRows / 16; ++i) {
+    for (int i = 0; i < kExpandRows / 32; ++i) {
       const int item = i * 256 + threadIdx.x;
-      const int r = item / 16, j = item % 16;
+      const int r = item / 8, j = item % 8;
       if (row0 + r >= p.m) continue;
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p.a_q + at + r * p.k + 8 * j));
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p.a_q + at + r * p.k + 16 * j));
       const float s = p.s_a != nullptr ? __ldg(p.s_a + row0 + r) : 1.0f;
-      uint32_t w[4];
+      const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+      uint32_t w[8];
 #pragma unroll
-      for (int h = 0; h < 4; ++h) {
-        const float2 f =
-            fp8_pair_to_float(((h < 2 ? v.x : v.y) >> (16 * (h % 2))) & 0xFFFFu, p.a_fmt);
+      for (int h = 0; h < 8; ++h) {
+        const float2 f = fp8_pair_to_float((in[h / 2] >> (16 * (h % 2))) & 0xFFFFu, p.a_fmt);
         w[h] = bf16_pair(f.x * s, f.y * s);
       }
-      *reinterpret_cast<uint4*>(p.xhat + at + r * p.k + 8 * j) =
-          make_uint4(w[0], w[1], w[2], w[3]);
+      store_sector(p.xhat + at + r * p.k + 16 * j, w);
     }
   }
 }

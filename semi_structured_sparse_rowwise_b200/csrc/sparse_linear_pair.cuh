@@ -70,9 +70,10 @@ constexpr int kPairMetaCol = 2 * kPairMaxTokens;  // after the two accumulators
 //   WT = 2: pair tile 512 x BN, one accumulator per weight slot (single
 //           buffer): each activation byte loaded feeds twice the MMAs.
 // The gated epilogues evaluate an activation per pair of accumulator rows, so
-// they get 16 warps however many weight slots there are (with 8, the gradient
-// epilogue took 1071 us of a tile loop whose MMAs take about 500: m = 8192,
-// k = 4096, 2n = 28672).
+// they get 16 warps however many weight slots there are: of 8 and 16, forward
+// 74 and 66 us at m = 4096, k = 2048, 2n = 11264, 488 and 505 us at m = 8192,
+// k = 4096, 2n = 28672 (where the MMAs of a tile hide more of it); gradient
+// 111 and 109, 600 and 572 us.
 template <int KS, int WT, int EPI = kEpiLinear>
 struct PairCfg {
   static_assert(KS == 1 || KS == 2, "1 or 2 k steps per stage");
