@@ -570,8 +570,10 @@ sfp8_status sfp8_gated_linear_backward(const void* dh, int64_t ld_dh, const void
  * x's type, or both in one call.
  *     mean = sum_c x / cols,   rstd = 1 / sqrt(sum_c (x - mean)^2 / cols + eps)
  *     y    = (x - mean) * rstd * weight + bias                  (fp32)
- *     codes and scales: those of sfp8_quantize_rowwise for the fp32 y (not for
- *     y after its rounding to x's type)
+ *     s    = max(max_c |y|, 1e-12f) / FP8_MAX,   q = RNE_satfinite_fp8(y * RN(1 / s))
+ * The codes are taken from the fp32 y, not from y after its rounding to x's
+ * type, and by the rounded reciprocal of s (sfp8_quantize_rowwise divides): a
+ * y next to a border of the format may fall on either side of it.
  *
  *  x       device, [rows, cols] of x_dtype (BF16, F16 or F32), row stride
  *          ld_x >= cols.  cols >= 1, any; with q, cols % 16 == 0 and x as for

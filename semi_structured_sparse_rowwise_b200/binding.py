@@ -651,8 +651,15 @@ def _like(x, t, what, dtype):
     return t
 
 
+_WIDE_CODE = {t: DTYPE[name] for t, name in TORCH_WIDE.items()}
+_FP8_CODE = {"e4m3": DTYPE["e4m3"], "e5m2": DTYPE["e5m2"]}
+
+
 def _fp8(dtype):
-    return DTYPE[_fp8_name(dtype)]
+    code = _FP8_CODE.get(dtype)
+    if code is None:
+        raise ValueError("fp8 dtype must be 'e4m3' or 'e5m2'")
+    return code
 
 
 def _activation(act):
@@ -679,8 +686,8 @@ def _out(t, what, shape, dtype, device):
 
 def _rows_in(x, what, cols=None):
     """A 2-D CUDA input with unit column stride: its type's code, its row stride."""
-    dtype = TORCH_WIDE.get(x.dtype)
-    if dtype is None:
+    code = _WIDE_CODE.get(x.dtype)
+    if code is None:
         raise ValueError("%s dtype must be bfloat16, float16 or float32" % what)
     if not x.is_cuda or x.dim() != 2 or (cols is not None and x.shape[1] != cols):
         raise ValueError("%s must be a 2-D CUDA tensor%s"
@@ -688,7 +695,7 @@ def _rows_in(x, what, cols=None):
     ld, unit = x.stride()
     if unit != 1 and x.shape[1] > 1:
         raise ValueError("%s must have unit column stride" % what)
-    return DTYPE[dtype], ld if x.shape[0] > 1 else x.shape[1]
+    return code, ld if x.shape[0] > 1 else x.shape[1]
 
 
 def _weight(packed, s_w, rows, k, device):
@@ -746,8 +753,8 @@ def sfp8_prepare_gated_weight_24(w_gate, w_up, q_dtype="e4m3", packed=None, scal
     if scales is None:
         scales = torch.empty((2 * n,), dtype=torch.float32, device=dev)
     _weight(packed, scales, 2 * n, k, dev)
-    _run("sfp8_prepare_gated_weight_24", dev, _addr(w_gate), _addr(w_up), wd, n, k, ld,
-         _fp8(q_dtype), _addr(packed), _addr(scales))
+    _run("sfp8_prepare_gated_weight_24", dev, w_gate.data_ptr(), w_up.data_ptr(), wd, n, k, ld,
+         _fp8(q_dtype), packed.data_ptr(), _addr(scales))
     return packed, scales
 
 
@@ -778,8 +785,9 @@ def sfp8_gated_linear(a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k, act="silu",
     out = _out(out, "out", (m, n), torch.bfloat16, dev)
     if workspace is None:
         workspace = new_gated_workspace(m, n, k, dev)
-    _run("sfp8_gated_linear", dev, _addr(a_q), _fp8(a_dtype), _addr(s_a), m, _addr(packed),
-         _fp8(w_dtype), _addr(s_w), n, k, _activation(act), _addr(bias), _addr(out),
+    _run("sfp8_gated_linear", dev, a_q.data_ptr(), _fp8(a_dtype), s_a.data_ptr(), m,
+         packed.data_ptr(), _fp8(w_dtype), s_w.data_ptr(), n, k, _activation(act), _addr(bias),
+         out.data_ptr(),
          *_workspace(workspace, dev))
     return out
 
@@ -797,9 +805,9 @@ def sfp8_gated_linear_quant(x, a_dtype, packed, w_dtype, s_w, n, k, act="silu", 
     s_a = _out(s_a, "s_a", (m,), torch.float32, dev)
     if workspace is None:
         workspace = new_gated_quant_workspace(m, n, k, dev)
-    _run("sfp8_gated_linear_quant", dev, _addr(x), xd, ld, _fp8(a_dtype), _addr(a_q), _addr(s_a),
-         m, _addr(packed), _fp8(w_dtype), _addr(s_w), n, k, _activation(act), _addr(bias),
-         _addr(out), *_workspace(workspace, dev))
+    _run("sfp8_gated_linear_quant", dev, x.data_ptr(), xd, ld, _fp8(a_dtype), a_q.data_ptr(),
+         s_a.data_ptr(), m, packed.data_ptr(), _fp8(w_dtype), s_w.data_ptr(), n, k,
+         _activation(act), _addr(bias), out.data_ptr(), *_workspace(workspace, dev))
     return out, a_q, s_a
 
 
@@ -844,9 +852,9 @@ def sfp8_sparse_linear_backward(dy, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, 
     dbias = _gradient(dbias, need_dbias, "dbias", (n,), dev)
     if workspace is None:
         workspace = new_linear_backward_workspace(m, n, k, dev)
-    _run("sfp8_sparse_linear_backward", dev, _addr(dy), ld, _addr(a_q), _fp8(a_dtype),
-         _addr(s_a), m, _addr(packed), _fp8(w_dtype), _addr(s_w), n, k, _addr(dx), _addr(dw),
-         _addr(dbias), *_workspace(workspace, dev))
+    _run("sfp8_sparse_linear_backward", dev, dy.data_ptr(), ld, a_q.data_ptr(), _fp8(a_dtype),
+         s_a.data_ptr(), m, packed.data_ptr(), _fp8(w_dtype), s_w.data_ptr(), n, k, _addr(dx),
+         _addr(dw), _addr(dbias), *_workspace(workspace, dev))
     return dx, dw, dbias
 
 
@@ -865,9 +873,10 @@ def sfp8_gated_linear_backward(dh, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k
     dbias = _gradient(dbias, need_dbias, "dbias", (2 * n,), dev)
     if workspace is None:
         workspace = new_gated_backward_workspace(m, n, k, dev)
-    _run("sfp8_gated_linear_backward", dev, _addr(dh), ld, _addr(a_q), _fp8(a_dtype), _addr(s_a),
-         m, _addr(packed), _fp8(w_dtype), _addr(s_w), n, k, _activation(act), _addr(bias),
-         _addr(dx), _addr(dw), _addr(dbias), *_workspace(workspace, dev))
+    _run("sfp8_gated_linear_backward", dev, dh.data_ptr(), ld, a_q.data_ptr(), _fp8(a_dtype),
+         s_a.data_ptr(), m, packed.data_ptr(), _fp8(w_dtype), s_w.data_ptr(), n, k,
+         _activation(act), _addr(bias), _addr(dx), _addr(dw), _addr(dbias),
+         *_workspace(workspace, dev))
     return dx, dw, dbias
 
 
@@ -880,8 +889,8 @@ def _norm_param(t, what, x):
         return None
     if t.dtype != x.dtype and t.dtype != torch.float32:
         raise ValueError("%s must have x's dtype or float32" % what)
-    _tensor(t, what, (x.shape[1],), t.dtype, x.device)
-    return DTYPE[TORCH_WIDE[t.dtype]]
+    _tensor(t, what, x.shape[1:], t.dtype, x.device)
+    return _WIDE_CODE[t.dtype]
 
 
 def _norm_forward(x, weight, bias, eps, out, q, q_dtype, scales, mean, rstd):
@@ -891,8 +900,9 @@ def _norm_forward(x, weight, bias, eps, out, q, q_dtype, scales, mean, rstd):
         raise ValueError("weight and bias must have the same dtype")
     rows, cols = x.shape
     pd = pd if pd is not None else bd if bd is not None else xd
-    _run("sfp8_layernorm", x.device, _addr(x), xd, rows, cols, ld, _addr(weight), _addr(bias), pd,
-         eps, _addr(out), _addr(q), _fp8(q_dtype), _addr(scales), _addr(mean), _addr(rstd))
+    _run("sfp8_layernorm", x.device, x.data_ptr(), xd, rows, cols, ld, _addr(weight),
+         _addr(bias), pd, eps, _addr(out), _addr(q), _fp8(q_dtype), _addr(scales), _addr(mean),
+         _addr(rstd))
 
 
 def _row_vectors(rows, device, *given):
@@ -960,9 +970,9 @@ def sfp8_layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, db
     dbias = _out(dbias, "dbias", (cols,), torch.float32, dev)
     if workspace is None:
         workspace = new_layernorm_backward_workspace(rows, cols, dev)
-    _run("sfp8_layernorm_backward", dev, _addr(dy), ld_dy, _addr(x), xd, rows, cols, ld_x,
+    _run("sfp8_layernorm_backward", dev, dy.data_ptr(), ld_dy, x.data_ptr(), xd, rows, cols, ld_x,
          _addr(weight), xd if pd is None else pd, _addr(mean), _addr(rstd), _addr(dx),
-         _addr(dweight), _addr(dbias), *_workspace(workspace, dev))
+         dweight.data_ptr(), _addr(dbias), *_workspace(workspace, dev))
     return dx, dweight, dbias
 
 

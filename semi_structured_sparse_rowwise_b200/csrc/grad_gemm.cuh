@@ -42,6 +42,11 @@
 //
 // Rows and columns past the operands' ends are filled with zeros by TMA and
 // never stored.  Every wait is bounded (device_common.cuh).
+//
+// Both products of m = 8192, r = 28672, k = 4096: 2.57 ms, 1.50 PFLOP/s, the
+// tensor pipe 98 % busy; of m = 2048, r = k = 4096: 88 us, 1.56 PFLOP/s.  The
+// epilogue's last tile is exposed, so its stores count at small sizes: whole
+// 32-byte sectors took m = 777, r = 1003, k = 1536 from 17.9 to 15.1 us.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -383,7 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
       int mt, nt, sp;
       gg_item(pr, index, mt, nt, sp);
       const int r = mt * kGgTileM + static_cast<int>(rank) * 128 + q * 32 + lane;
-      const float rs = pr.row_scale != nullptr && r < pr.rows ? 1.0f / __ldg(pr.row_scale + r) : 1.0f;
+      const float rs =
+          pr.row_scale != nullptr && r < pr.rows ? 1.0f / __ldg(pr.row_scale + r) : 1.0f;
       int ok = 1;
       if (lane == 0) ok = mbar_wait(smem_u32(&accf_bar[acc]), acc_phase, abort_flag) ? 1 : 0;
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -459,8 +465,8 @@ struct JoinParams {
 };
 
 // D = the sum of the splits' partial sums, in split order, scaled and rounded
-// once (one thread per 8 columns; D's columns are a multiple of 128); then, in blocks of their own, the bias
-// gradient: 32 columns a block, each of 8 row lanes adding every eighth run,
+// once (one thread per 8 columns; D's columns are a multiple of 128); then, in
+// blocks of their own, the bias gradient: 32 columns a block, each of 8 row lanes adding every eighth run,
 // the lanes added in order.
 __global__ void __launch_bounds__(256) backward_join_kernel(const __grid_constant__ JoinParams p) {
   grid_dependents_launch();
@@ -678,7 +684,8 @@ __device__ __forceinline__ void sum_columns(const PrologueParams& p, int block,
     for (long long r = r0 + ty; r < r1; r += 8) {
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (first + j * step < p.rows) s[j] += __bfloat162float(p.dy[r * p.ld_dy + first + j * step]);
+        if (first + j * step < p.rows)
+          s[j] += __bfloat162float(p.dy[r * p.ld_dy + first + j * step]);
     }
   }
 #pragma unroll

@@ -13,8 +13,9 @@
 // All of it in fp32; y and dx are rounded once to x's type, the codes once
 // from the fp32 y (multiplied by the rounded reciprocal of s, where the
 // quantiser of a given tensor divides: the fp32 y is itself a few roundings
-// off, so the quotient's last bit decides nothing).  The variance is taken about the mean (two reductions over
-// values held in registers), never as a difference of two sums.
+// off, so the quotient's last bit decides nothing).  The variance is taken
+// about the mean (two reductions over values held in registers), never as a
+// difference of two sums.
 //
 // Both passes are bound by memory.  Kernels by row length and count:
 //   row kernel     few rows (or short ones): one row per group of TPR threads,
