@@ -466,8 +466,8 @@ struct JoinParams {
 
 // D = the sum of the splits' partial sums, in split order, scaled and rounded
 // once (one thread per 8 columns; D's columns are a multiple of 128); then, in
-// blocks of their own, the bias gradient: 32 columns a block, each of 8 row lanes adding every eighth run,
-// the lanes added in order.
+// blocks of their own, the bias gradient: 32 columns a block, each of 8 row
+// lanes adding every eighth run, the lanes added in order.
 __global__ void __launch_bounds__(256) backward_join_kernel(const __grid_constant__ JoinParams p) {
   grid_dependents_launch();
   grid_dependency_wait();

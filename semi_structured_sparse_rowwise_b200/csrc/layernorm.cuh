@@ -361,7 +361,8 @@ struct NormRing {
   // finished with.
   __device__ void fill(int slot, const void* a, const void* b) const {
     const uint32_t bar = smem_u32(&full[slot]);
-    const uint64_t pol = l2_policy_evict_first();
+    // x and dy are read again by others (a residual addition, the backward pass)
+    const uint64_t pol = l2_policy_evict_normal();
     uint8_t* dst = buffer(slot);
     mbar_arrive_expect_tx(bar, PARTS * bytes);
     bulk_load(smem_u32(dst), a, bytes, bar, pol);

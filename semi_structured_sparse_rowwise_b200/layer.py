@@ -192,11 +192,16 @@ class SparseFp8GatedLinear:
         self._ws = {}
 
     def _workspace(self, kind, m):
+        if kind == "backward":
+            return _kept(self._ws, (kind, m), B.new_gated_backward_workspace, m, self.n, self.k,
+                         self.device)
         # a changed algorithm table may ask for another size
-        new = {"quant": B.new_gated_quant_workspace, "codes": B.new_gated_workspace,
-               "backward": B.new_gated_backward_workspace}[kind]
-        epoch = 0 if kind == "backward" else B.algo_epoch()
-        return _kept(self._ws, (kind, m, epoch), new, m, self.n, self.k, self.device)
+        epoch = B.algo_epoch()
+        hit = self._ws.get((kind, m))
+        if hit is None or hit[0] != epoch:
+            new = B.new_gated_quant_workspace if kind == "quant" else B.new_gated_workspace
+            hit = self._ws[(kind, m)] = (epoch, new(m, self.n, self.k, self.device))
+        return hit[1]
 
     def forward_checkpoint(self, x, out=None):
         """(h [m, hidden] bf16, checkpoint) from x [m, k] bf16/f16/f32; the

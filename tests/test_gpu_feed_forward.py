@@ -96,6 +96,22 @@ def test_gated_layer_is_its_calls():
     assert layer.backward(dh, (a_q, s_a), need_dx=False, need_dbias=False)[0::2] == (None, None)
 
 
+def test_gated_layer_follows_the_algorithm_table():
+    k, hidden, m = 1024, 320, 16
+    w = weights(k, hidden, 8)
+    layer = S.SparseFp8GatedLinear(w["w_gate"], w["w_up"])
+    x = torch.randn(m, k, device="cuda", generator=gen(4)).to(torch.bfloat16)
+    want = layer(x)
+    try:
+        for algo in range(S.sfp8_sparse_linear_algo_count(m, 2 * hidden, k)):
+            S.sfp8_sparse_linear_set_algo(m, 2 * hidden, k, algo)
+            for _ in range(2):
+                near(layer(x), want.double(), 1)
+        assert len(layer._ws) == 1      # one workspace, however often the table changed
+    finally:
+        S.sfp8_sparse_linear_set_algo(m, 2 * hidden, k, 0)
+
+
 def test_linear_layer_backward():
     layer = S.SparseFp8Linear(torch.randn(96, 256, device="cuda", generator=gen(1)) * 0.1,
                               bias=torch.zeros(96, device="cuda"))
