@@ -205,7 +205,7 @@ template <typename T>
 sfp8_status launch_norm_grad(DeviceInfo* dev, int kind, NormGradParams& p, bool vec, bool sums,
                              cudaStream_t st) {
   constexpr int V = InputTraits<T>::kPerVec;
-  const int s0 = 36 + kind * 8;
+  const int s0 = 36 + kind * 12;
   if (vec) {
     const int nvec = p.cols / V;
     if (nvec <= 32) return launch_norm_grad_rows<T, V, 32, 1>(dev, s0, p, st);
@@ -213,10 +213,22 @@ sfp8_status launch_norm_grad(DeviceInfo* dev, int kind, NormGradParams& p, bool 
     auto go = [&](int slot, auto kern, int threads, int per_block) {
       return launch_norm_grad_stream<T>(dev, s0 + slot, kern, threads, per_block, p, st);
     };
-    if (nvec <= 128) return go(2, layernorm_backward_stream_kernel<T, V, 128, 1, 768>, 768, 6);
-    if (nvec <= 256) return go(3, layernorm_backward_stream_kernel<T, V, 128, 2, 640>, 640, 5);
-    if (nvec <= 512) return go(4, layernorm_backward_stream_kernel<T, V, 128, 4, 512>, 512, 4);
-    if (nvec <= 1024) return go(5, layernorm_backward_stream_kernel<T, V, 256, 4, 512>, 512, 2);
+    if (nvec == 128)
+      return go(8, layernorm_backward_stream_kernel<T, V, 128, 1, 768, true>, 768, 6);
+    if (nvec == 256)
+      return go(9, layernorm_backward_stream_kernel<T, V, 128, 2, 640, true>, 640, 5);
+    if (nvec == 512)
+      return go(10, layernorm_backward_stream_kernel<T, V, 128, 4, 512, true>, 512, 4);
+    if (nvec == 1024)
+      return go(11, layernorm_backward_stream_kernel<T, V, 256, 4, 512, true>, 512, 2);
+    if (nvec <= 128)
+      return go(2, layernorm_backward_stream_kernel<T, V, 128, 1, 768, false>, 768, 6);
+    if (nvec <= 256)
+      return go(3, layernorm_backward_stream_kernel<T, V, 128, 2, 640, false>, 640, 5);
+    if (nvec <= 512)
+      return go(4, layernorm_backward_stream_kernel<T, V, 128, 4, 512, false>, 512, 4);
+    if (nvec <= 1024)
+      return go(5, layernorm_backward_stream_kernel<T, V, 256, 4, 512, false>, 512, 2);
   } else {
     if (p.cols <= 1024) return launch_norm_grad_rows<T, 1, 128, 8>(dev, s0 + 6, p, st);
     if (p.cols <= 4096) return launch_norm_grad_rows<T, 1, 512, 8>(dev, s0 + 7, p, st);

@@ -37,7 +37,7 @@ struct DeviceInfo {
   int pair_clusters[12] = {};    // co-resident pairs of the pair kernel by (KS, WT) and epilogue
                                  // (0: unknown)
   int grad_clusters[4] = {};     // the same of the gradient GEMM by (tile width, A's major-ness)
-  int norm_blocks[64] = {};      // co-resident CTAs per SM of the persistent layer norm kernels
+  int norm_blocks[72] = {};      // co-resident CTAs per SM of the persistent layer norm kernels
                                  // by (direction, type, row split) (0: unknown)
   int tw_blocks[12] = {};        // co-resident CTAs per SM of the tensor-wise quantiser (0: unknown)
   long long l2_bytes = 0;
