@@ -183,6 +183,29 @@ def test_repeats_bit_for_bit_and_shares_a_workspace():
         assert all(torch.equal(a, b) for a, b in zip(first, again))
 
 
+@pytest.mark.parametrize("m,n,k", [(60, 300, 256), (640, 2000, 512)])
+def test_calls_that_follow_each_other_on_one_workspace(m, n, k):
+    """Passes over different operands, one after the other without a wait, in
+    one workspace: each must find the one before it done with the expanded
+    operands and dz that it overwrites."""
+    ops = [operands(m, 2 * n, k, 20 + i) for i in range(2)]
+    dhs = [torch.randn(m, n, device="cuda", generator=gen(i)).to(torch.bfloat16) for i in range(2)]
+    ws = S.new_gated_backward_workspace(m, n, k, "cuda")
+
+    def run(i, workspace):
+        a_q, s_a, _, s_w, packed = ops[i]
+        return S.sfp8_gated_linear_backward(dhs[i], a_q, "e4m3", s_a, packed, "e4m3", s_w, n, k,
+                                            need_dbias=True, workspace=workspace)
+
+    want = []
+    for i in range(2):
+        want.append(run(i, S.new_gated_backward_workspace(m, n, k, "cuda")))
+        torch.cuda.synchronize()
+    got = [run(i % 2, ws) for i in range(40)]
+    for i, g in enumerate(got):
+        assert all(torch.equal(a, b) for a, b in zip(g, want[i % 2])), i
+
+
 def test_outputs_and_workspaces_at_any_allowed_alignment():
     """16-byte aligned gradients and workspaces that are not 32-byte aligned,
     with a split contraction (few rows of dx, many weight rows)."""
