@@ -611,12 +611,19 @@ def _quant_linear(name, x, a_dtype, packed, w_dtype, s_w, n, k, bias, out, works
 
 # ---------------------------------------------------------------- feed-forward sublayer
 # The wrappers below are called once a layer and token in serving, where the
-# host's share of a call is as long as its kernels.  They pass plain integers
-# for pointers and read the device and the raw stream directly: together with
-# the checks about 10 us a call, where torch's device context manager, stream
-# object and ctypes pointer objects alone take that long.
+# host's share of a call is as long as its kernels (on a B200 host: 4 us in the
+# library, 1.3 to 2.3 us for each result that torch allocates, and what
+# Python adds).  So they check their arguments in few, flat expressions that only a
+# refusal takes apart again, pass plain integers for pointers and read the
+# device and the raw stream directly; torch's device context manager, stream
+# object and ctypes pointer objects alone would take 10 us more.
 
-
+# absent from a torch without CUDA, which still imports this module
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_U8, _F32, _BF16 = torch.uint8, torch.float32, torch.bfloat16
+_WIDE_CODE = {t: DTYPE[name] for t, name in TORCH_WIDE.items()}
+_FP8_CODE = {"e4m3": DTYPE["e4m3"], "e5m2": DTYPE["e5m2"]}
 _FN = {}
 
 
@@ -627,32 +634,17 @@ def _run(name, device, *args):
     if fn is None:
         fn = _FN[name] = getattr(load_library(), name)
     index = device.index
-    if torch._C._cuda_getDevice() == index:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    if _get_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(index))
+            status = fn(*args, _raw_stream(index))
     if status != OK:
         raise Sfp8Error(status, name)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
-
-
-def _like(x, t, what, dtype):
-    """A contiguous output of x's shape: given (checked) or new (empty_like is
-    the cheaper call where it gives that)."""
-    if t is None:
-        if x.is_contiguous():
-            return torch.empty_like(x, dtype=dtype)
-        return torch.empty(x.shape, dtype=dtype, device=x.device)
-    _tensor(t, what, x.shape, dtype, x.device)
-    return t
-
-
-_WIDE_CODE = {t: DTYPE[name] for t, name in TORCH_WIDE.items()}
-_FP8_CODE = {"e4m3": DTYPE["e4m3"], "e5m2": DTYPE["e5m2"]}
 
 
 def _fp8(dtype):
@@ -663,9 +655,10 @@ def _fp8(dtype):
 
 
 def _activation(act):
-    if act not in ACTIVATION:
+    code = ACTIVATION.get(act)
+    if code is None:
         raise ValueError("act must be 'silu' or 'gelu'")
-    return ACTIVATION[act]
+    return code
 
 
 def _tensor(t, what, shape, dtype, device):
@@ -676,47 +669,52 @@ def _tensor(t, what, shape, dtype, device):
                          % (what, dtype, tuple(shape), device))
 
 
-def _out(t, what, shape, dtype, device):
-    """A given output, checked, or a new one."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _tensor(t, what, shape, dtype, device)
-    return t
+def _like(x, t, what, dtype):
+    """A contiguous output of x's shape: given (checked) or new (empty_like is
+    the cheaper call where it gives that)."""
+    if t is not None:
+        _tensor(t, what, x.shape, dtype, x.device)
+        return t
+    return torch.empty_like(x, dtype=dtype) if x.is_contiguous() else x.new_empty(x.shape,
+                                                                                 dtype=dtype)
 
 
 def _rows_in(x, what, cols=None):
-    """A 2-D CUDA input with unit column stride: its type's code, its row stride."""
+    """A 2-D CUDA input with unit column stride (and `cols` columns): the code
+    of its type, its rows, columns and row stride."""
     code = _WIDE_CODE.get(x.dtype)
-    if code is None:
-        raise ValueError("%s dtype must be bfloat16, float16 or float32" % what)
-    if not x.is_cuda or x.dim() != 2 or (cols is not None and x.shape[1] != cols):
-        raise ValueError("%s must be a 2-D CUDA tensor%s"
-                         % (what, "" if cols is None else " with %d columns" % cols))
+    shape = x.shape
+    if code is None or not x.is_cuda or len(shape) != 2:
+        raise ValueError("%s must be a 2-D CUDA tensor of bfloat16, float16 or float32" % what)
+    rows, width = shape
     ld, unit = x.stride()
-    if unit != 1 and x.shape[1] > 1:
-        raise ValueError("%s must have unit column stride" % what)
-    return code, ld if x.shape[0] > 1 else x.shape[1]
+    if (unit != 1 and width > 1) or (cols is not None and width != cols):
+        raise ValueError("%s must have unit column stride%s"
+                         % (what, "" if cols is None else " and %d columns" % cols))
+    return code, rows, width, ld if rows > 1 else width
 
 
 def _weight(packed, s_w, rows, k, device):
     """The compressed weight of `rows` rows and its scales, on `device`."""
-    if rows < 0 or k < 0:
-        raise ValueError("n and k must not be negative")
     need = (rows + 127) // 128 * 128 * k * 5 // 8
-    if (packed.device != device or packed.dtype != torch.uint8 or not packed.is_contiguous()
-            or packed.numel() < need):
-        raise ValueError("packed must be a contiguous uint8 tensor of at least %d bytes on %s"
-                         % (need, device))
-    _tensor(s_w, "s_w", (rows,), torch.float32, device)
+    if (rows < 0 or k < 0 or packed.dtype != _U8 or packed.device != device
+            or not packed.is_contiguous() or packed.numel() < need):
+        raise ValueError("packed must be a contiguous uint8 tensor of at least %d bytes on %s "
+                         "(n and k not negative)" % (need, device))
+    if (s_w.shape != (rows,) or s_w.dtype != _F32 or s_w.device != device
+            or not s_w.is_contiguous()):
+        _tensor(s_w, "s_w", (rows,), _F32, device)
 
 
 def _codes(a_q, s_a, k):
     """A quantised activation [m, k] and its scales: its rows and device."""
-    if not a_q.is_cuda or a_q.dim() != 2:
-        raise ValueError("a_q must be a 2-D CUDA tensor")
-    m, dev = a_q.shape[0], a_q.device
-    _tensor(a_q, "a_q", (m, k), torch.uint8, dev)
-    _tensor(s_a, "s_a", (m,), torch.float32, dev)
+    shape = a_q.shape
+    if (len(shape) != 2 or shape[1] != k or a_q.dtype != _U8 or not a_q.is_cuda
+            or not a_q.is_contiguous()):
+        raise ValueError("a_q must be a contiguous uint8 CUDA tensor [m, k=%d]" % k)
+    m, dev = shape[0], a_q.device
+    if s_a.shape != (m,) or s_a.dtype != _F32 or s_a.device != dev or not s_a.is_contiguous():
+        _tensor(s_a, "s_a", (m,), _F32, dev)
     return m, dev
 
 
@@ -741,12 +739,10 @@ def sfp8_prepare_gated_weight_24(w_gate, w_up, q_dtype="e4m3", packed=None, scal
     """w_gate, w_up [n, k] bf16/f16/f32 (unit column stride, the same type and
     strides) -> (packed, s_w): the compressed weight of a gated block, 2n rows
     that alternate gate and up, each prepared as by sfp8_prepare_weight_24."""
-    wd, ld = _rows_in(w_gate, "w_gate")
-    if (w_up.shape != w_gate.shape or w_up.dtype != w_gate.dtype or w_up.device != w_gate.device
-            or _rows_in(w_up, "w_up")[1] != ld):
-        raise ValueError("w_up must have w_gate's shape, dtype, device and strides")
-    n, k = w_gate.shape
+    wd, n, k, ld = _rows_in(w_gate, "w_gate")
     dev = w_gate.device
+    if w_up.device != dev or _rows_in(w_up, "w_up") != (wd, n, k, ld):
+        raise ValueError("w_up must have w_gate's shape, dtype, device and strides")
     if packed is None:
         packed = torch.empty((load_library().sfp8_compressed_bytes(2 * n, k),),
                              dtype=torch.uint8, device=dev)
@@ -754,7 +750,7 @@ def sfp8_prepare_gated_weight_24(w_gate, w_up, q_dtype="e4m3", packed=None, scal
         scales = torch.empty((2 * n,), dtype=torch.float32, device=dev)
     _weight(packed, scales, 2 * n, k, dev)
     _run("sfp8_prepare_gated_weight_24", dev, w_gate.data_ptr(), w_up.data_ptr(), wd, n, k, ld,
-         _fp8(q_dtype), packed.data_ptr(), _addr(scales))
+         _fp8(q_dtype), packed.data_ptr(), scales.data_ptr())
     return packed, scales
 
 
@@ -769,26 +765,24 @@ def new_gated_quant_workspace(m, n, k, device):
                           device)
 
 
-def _gated_weight(n, k, packed, s_w, bias, device):
-    _weight(packed, s_w, 2 * n, k, device)
-    if bias is not None:
-        _tensor(bias, "bias", (2 * n,), torch.bfloat16, device)
-
-
 def sfp8_gated_linear(a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k, act="silu", bias=None,
                       out=None, workspace=None):
     """h [m, n] bf16 = act(gate) * up of a quantised activation a_q [m, k],
     s_a [m]; packed, s_w from sfp8_prepare_gated_weight_24, bias [2n] bf16
     (gate's n values, then up's)."""
     m, dev = _codes(a_q, s_a, k)
-    _gated_weight(n, k, packed, s_w, bias, dev)
-    out = _out(out, "out", (m, n), torch.bfloat16, dev)
+    _weight(packed, s_w, 2 * n, k, dev)
+    if bias is not None:
+        _tensor(bias, "bias", (2 * n,), _BF16, dev)
+    if out is None:
+        out = a_q.new_empty((m, n), dtype=_BF16)
+    else:
+        _tensor(out, "out", (m, n), _BF16, dev)
     if workspace is None:
         workspace = new_gated_workspace(m, n, k, dev)
     _run("sfp8_gated_linear", dev, a_q.data_ptr(), _fp8(a_dtype), s_a.data_ptr(), m,
          packed.data_ptr(), _fp8(w_dtype), s_w.data_ptr(), n, k, _activation(act), _addr(bias),
-         out.data_ptr(),
-         *_workspace(workspace, dev))
+         out.data_ptr(), *_workspace(workspace, dev))
     return out
 
 
@@ -797,12 +791,20 @@ def sfp8_gated_linear_quant(x, a_dtype, packed, w_dtype, s_w, n, k, act="silu", 
     """Quantise x [m, k] (bf16/f16/f32, unit column stride) row-wise and apply
     the gated block, one library call: returns (h [m, n] bf16, a_q [m, k]
     uint8, s_a [m] f32); a_q and s_a are what the backward pass needs."""
-    xd, ld = _rows_in(x, "x", k)
-    m, dev = x.shape[0], x.device
-    _gated_weight(n, k, packed, s_w, bias, dev)
-    out = _out(out, "out", (m, n), torch.bfloat16, dev)
-    a_q = _like(x, a_q, "a_q", torch.uint8)
-    s_a = _out(s_a, "s_a", (m,), torch.float32, dev)
+    xd, m, _, ld = _rows_in(x, "x", k)
+    dev = x.device
+    _weight(packed, s_w, 2 * n, k, dev)
+    if bias is not None:
+        _tensor(bias, "bias", (2 * n,), _BF16, dev)
+    if out is None:
+        out = x.new_empty((m, n), dtype=_BF16)
+    else:
+        _tensor(out, "out", (m, n), _BF16, dev)
+    a_q = _like(x, a_q, "a_q", _U8)
+    if s_a is None:
+        s_a = s_w.new_empty(m)
+    else:
+        _tensor(s_a, "s_a", (m,), _F32, dev)
     if workspace is None:
         workspace = new_gated_quant_workspace(m, n, k, dev)
     _run("sfp8_gated_linear_quant", dev, x.data_ptr(), xd, ld, _fp8(a_dtype), a_q.data_ptr(),
@@ -826,15 +828,19 @@ def new_gated_backward_workspace(m, n, k, device):
                           device)
 
 
-def _gradient(t, wanted, what, shape, device):
-    """A gradient asked for: given (checked) or new; None where it is not."""
-    return _out(t, what, shape, torch.bfloat16, device) if wanted or t is not None else None
+def _gradient(t, wanted, what, shape, like):
+    """A bf16 gradient asked for: given (checked) or new; None where it is not."""
+    if t is not None:
+        _tensor(t, what, shape, _BF16, like.device)
+        return t
+    return like.new_empty(shape) if wanted else None
 
 
 def _grad_in(dy, what, m, n, device):
-    if dy.shape != (m, n) or dy.dtype != torch.bfloat16 or dy.device != device:
+    """Row stride of the output's gradient [m, n] bf16, unit column stride."""
+    if dy.dtype != _BF16 or dy.shape != (m, n) or dy.device != device:
         raise ValueError("%s must be a bfloat16 tensor of shape %s on %s" % (what, (m, n), device))
-    return _rows_in(dy, what)[1]
+    return _rows_in(dy, what)[3]
 
 
 def sfp8_sparse_linear_backward(dy, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k, need_dx=True,
@@ -847,9 +853,9 @@ def sfp8_sparse_linear_backward(dy, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, 
     m, dev = _codes(a_q, s_a, k)
     _weight(packed, s_w, n, k, dev)
     ld = _grad_in(dy, "dy", m, n, dev)
-    dx = _gradient(dx, need_dx, "dx", (m, k), dev)
-    dw = _gradient(dw, need_dw, "dw", (n, k), dev)
-    dbias = _gradient(dbias, need_dbias, "dbias", (n,), dev)
+    dx = _gradient(dx, need_dx, "dx", (m, k), dy)
+    dw = _gradient(dw, need_dw, "dw", (n, k), dy)
+    dbias = _gradient(dbias, need_dbias, "dbias", (n,), dy)
     if workspace is None:
         workspace = new_linear_backward_workspace(m, n, k, dev)
     _run("sfp8_sparse_linear_backward", dev, dy.data_ptr(), ld, a_q.data_ptr(), _fp8(a_dtype),
@@ -866,11 +872,13 @@ def sfp8_gated_linear_backward(dh, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k
     dbias [2n]), bf16, None where not asked for; dw's and dbias's first n rows
     are gate's, the others up's."""
     m, dev = _codes(a_q, s_a, k)
-    _gated_weight(n, k, packed, s_w, bias, dev)
+    _weight(packed, s_w, 2 * n, k, dev)
+    if bias is not None:
+        _tensor(bias, "bias", (2 * n,), _BF16, dev)
     ld = _grad_in(dh, "dh", m, n, dev)
-    dx = _gradient(dx, need_dx, "dx", (m, k), dev)
-    dw = _gradient(dw, need_dw, "dw", (2 * n, k), dev)
-    dbias = _gradient(dbias, need_dbias, "dbias", (2 * n,), dev)
+    dx = _gradient(dx, need_dx, "dx", (m, k), dh)
+    dw = _gradient(dw, need_dw, "dw", (2 * n, k), dh)
+    dbias = _gradient(dbias, need_dbias, "dbias", (2 * n,), dh)
     if workspace is None:
         workspace = new_gated_backward_workspace(m, n, k, dev)
     _run("sfp8_gated_linear_backward", dev, dh.data_ptr(), ld, a_q.data_ptr(), _fp8(a_dtype),
@@ -883,51 +891,44 @@ def sfp8_gated_linear_backward(dh, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k
 # ---- layer norm
 
 
-def _norm_param(t, what, x):
-    """A weight or bias of x's dtype or float32; its dtype's code."""
-    if t is None:
-        return None
-    if t.dtype != x.dtype and t.dtype != torch.float32:
-        raise ValueError("%s must have x's dtype or float32" % what)
-    _tensor(t, what, x.shape[1:], t.dtype, x.device)
-    return _WIDE_CODE[t.dtype]
+def _norm_in(x, weight, bias):
+    """Checks layer norm's inputs: the codes of x's and the parameters' types, x's
+    rows, columns and row stride, its device."""
+    xd, rows, cols, ld = _rows_in(x, "x")
+    dtype, dev = x.dtype, x.device
+    pd = None
+    for t in (weight, bias):
+        if t is None:
+            continue
+        td = t.dtype
+        if ((td != dtype and td != _F32) or (pd is not None and td != pd) or t.shape != (cols,)
+                or t.device != dev or not t.is_contiguous()):
+            raise ValueError("weight and bias must be contiguous tensors of shape %s on %s, both "
+                             "of x's dtype or both float32" % ((cols,), dev))
+        pd = td
+    return xd, rows, cols, ld, xd if pd is None else _WIDE_CODE[pd], dev
 
 
-def _norm_forward(x, weight, bias, eps, out, q, q_dtype, scales, mean, rstd):
-    xd, ld = _rows_in(x, "x")
-    pd, bd = _norm_param(weight, "weight", x), _norm_param(bias, "bias", x)
-    if pd is not None and bd is not None and pd != bd:
-        raise ValueError("weight and bias must have the same dtype")
-    rows, cols = x.shape
-    pd = pd if pd is not None else bd if bd is not None else xd
-    _run("sfp8_layernorm", x.device, x.data_ptr(), xd, rows, cols, ld, _addr(weight),
-         _addr(bias), pd, eps, _addr(out), _addr(q), _fp8(q_dtype), _addr(scales), _addr(mean),
-         _addr(rstd))
-
-
-def _row_vectors(rows, device, *given):
-    """float32 [rows] outputs: the given ones (name, tensor) checked, the
-    others new."""
-    out = []
-    new = None
-    for what, t in given:
-        if t is not None:
-            _tensor(t, what, (rows,), torch.float32, device)
-        elif new is None:
-            t = new = torch.empty((rows,), dtype=torch.float32, device=device)
-        else:
-            t = torch.empty_like(new)     # the cheaper call
-        out.append(t)
-    return out
+def _row_vector(t, what, rows, dev, like=None):
+    """A float32 [rows] output: given (checked) or new."""
+    if t is not None:
+        _tensor(t, what, (rows,), _F32, dev)
+        return t
+    if like is None:
+        return torch.empty((rows,), dtype=_F32, device=dev)
+    return torch.empty_like(like)  # the cheaper call
 
 
 def sfp8_layernorm(x, weight=None, bias=None, eps=1e-5, out=None, mean=None, rstd=None):
     """Layer norm of x [rows, cols] bf16/f16/f32 (unit column stride), weight
     and bias [cols] of x's dtype or float32: returns (y of x's dtype, mean
     [rows], rstd [rows] float32)."""
+    xd, rows, cols, ld, pd, dev = _norm_in(x, weight, bias)
     out = _like(x, out, "out", x.dtype)
-    mean, rstd = _row_vectors(x.shape[0], x.device, ("mean", mean), ("rstd", rstd))
-    _norm_forward(x, weight, bias, eps, out, None, "e4m3", None, mean, rstd)
+    mean = _row_vector(mean, "mean", rows, dev)
+    rstd = _row_vector(rstd, "rstd", rows, dev, mean)
+    _run("sfp8_layernorm", dev, x.data_ptr(), xd, rows, cols, ld, _addr(weight), _addr(bias), pd,
+         eps, out.data_ptr(), None, _FP8_CODE["e4m3"], None, mean.data_ptr(), rstd.data_ptr())
     return out, mean, rstd
 
 
@@ -936,12 +937,16 @@ def sfp8_layernorm_quant(x, weight=None, bias=None, eps=1e-5, q_dtype="e4m3", q=
     """Layer norm of x straight to row-wise FP8 codes, the input of the linear
     and the gated block: returns (q [rows, cols] uint8, scales, mean, rstd
     [rows] float32).  A given `out` also receives y in x's dtype."""
-    q = _like(x, q, "q", torch.uint8)
+    xd, rows, cols, ld, pd, dev = _norm_in(x, weight, bias)
+    q = _like(x, q, "q", _U8)
     if out is not None:
-        _tensor(out, "out", x.shape, x.dtype, x.device)
-    scales, mean, rstd = _row_vectors(x.shape[0], x.device, ("scales", scales), ("mean", mean),
-                                      ("rstd", rstd))
-    _norm_forward(x, weight, bias, eps, out, q, q_dtype, scales, mean, rstd)
+        _tensor(out, "out", x.shape, x.dtype, dev)
+    scales = _row_vector(scales, "scales", rows, dev)
+    mean = _row_vector(mean, "mean", rows, dev, scales)
+    rstd = _row_vector(rstd, "rstd", rows, dev, scales)
+    _run("sfp8_layernorm", dev, x.data_ptr(), xd, rows, cols, ld, _addr(weight), _addr(bias), pd,
+         eps, _addr(out), q.data_ptr(), _fp8(q_dtype), scales.data_ptr(), mean.data_ptr(),
+         rstd.data_ptr())
     return q, scales, mean, rstd
 
 
@@ -956,23 +961,24 @@ def sfp8_layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, db
     """Gradients of layer norm from dy [rows, cols] (x's dtype) and the
     forward's x, weight (or None), mean and rstd: returns (dx of x's dtype,
     dweight, dbias [cols] float32)."""
-    xd, ld_x = _rows_in(x, "x")
-    dyd, ld_dy = _rows_in(dy, "dy")
-    dev = x.device
-    if dyd != xd or dy.shape != x.shape or dy.device != dev:
+    xd, rows, cols, ld_x, pd, dev = _norm_in(x, weight, None)
+    dyd, dy_rows, dy_cols, ld_dy = _rows_in(dy, "dy")
+    if dyd != xd or dy_rows != rows or dy_cols != cols or dy.device != dev:
         raise ValueError("dy must have x's shape, dtype and device")
-    pd = _norm_param(weight, "weight", x)
-    rows, cols = x.shape
-    _tensor(mean, "mean", (rows,), torch.float32, dev)
-    _tensor(rstd, "rstd", (rows,), torch.float32, dev)
+    for t, what in ((mean, "mean"), (rstd, "rstd")):
+        if t.shape != (rows,) or t.dtype != _F32 or t.device != dev or not t.is_contiguous():
+            _tensor(t, what, (rows,), _F32, dev)
     dx = _like(x, dx, "dx", x.dtype)
-    dweight = _out(dweight, "dweight", (cols,), torch.float32, dev)
-    dbias = _out(dbias, "dbias", (cols,), torch.float32, dev)
+    if dweight is None:
+        dweight = mean.new_empty(cols)
+    else:
+        _tensor(dweight, "dweight", (cols,), _F32, dev)
+    dbias = _row_vector(dbias, "dbias", cols, dev, dweight)
     if workspace is None:
         workspace = new_layernorm_backward_workspace(rows, cols, dev)
     _run("sfp8_layernorm_backward", dev, dy.data_ptr(), ld_dy, x.data_ptr(), xd, rows, cols, ld_x,
-         _addr(weight), xd if pd is None else pd, _addr(mean), _addr(rstd), _addr(dx),
-         dweight.data_ptr(), _addr(dbias), *_workspace(workspace, dev))
+         _addr(weight), pd, mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), dweight.data_ptr(),
+         dbias.data_ptr(), *_workspace(workspace, dev))
     return dx, dweight, dbias
 
 
