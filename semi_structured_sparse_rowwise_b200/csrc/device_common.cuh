@@ -404,10 +404,13 @@ __device__ __forceinline__ uint32_t map_to_cta(uint32_t addr, uint32_t rank) {
   return r;
 }
 
-// Arrive (release, cluster scope) on a barrier given by its shared::cluster
-// address, which may be in the other CTA of the pair.
+// Arrive on a barrier given by its shared::cluster address, which may be in the
+// other CTA of the pair, to hand back tensor memory that this warp's completed
+// tcgen05.ld (wait::ld, then fence::before_thread_sync) have read.  Relaxed:
+// nothing in shared or global memory goes with it.  A release at cluster scope
+// would first wait for the warp's global stores to arrive, once a tile.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(
                    cluster_addr)
                : "memory");
 }
