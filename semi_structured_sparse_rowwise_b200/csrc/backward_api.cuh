@@ -287,10 +287,11 @@ sfp8_status launch_linear_grads(DeviceInfo* dev, const BackwardPlan& bp, const B
       const int64_t d_rows = i == 0 ? c.m : c.rows;
       const int64_t contraction = i == 0 ? c.rows : c.m;
       const void* b = ws + (i == 0 ? bp.what_off : bp.xhat_off);
-      sfp8_status s = i == 0 ? encode_bf16_2d(&maps.a[at], dz, c.rows, c.m, ld, 128)
-                             : encode_bf16_2d(&maps.a[at], dz, c.rows, c.m, ld, kGgStageK);
+      pr.a_rows = c.m < 128 ? static_cast<int>((c.m + 7) / 8 * 8) : 128;
+      pr.t_rows = contraction < kGgStageK ? static_cast<int>((contraction + 15) / 16 * 16) : kGgStageK;
+      sfp8_status s = encode_bf16_2d(&maps.a[at], dz, c.rows, c.m, ld, i == 0 ? pr.a_rows : pr.t_rows);
       if (s != SFP8_OK) return s;
-      s = encode_bf16_2d(&maps.b[at], b, c.k, contraction, c.k, kGgStageK);
+      s = encode_bf16_2d(&maps.b[at], b, c.k, contraction, c.k, pr.t_rows);
       if (s != SFP8_OK) return s;
       pr.d = static_cast<__nv_bfloat16*>(i == 0 ? c.dx : c.dw);
       pr.partial = reinterpret_cast<float*>(ws + partial);

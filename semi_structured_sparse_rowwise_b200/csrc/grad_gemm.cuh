@@ -51,6 +51,8 @@
 
 #include <cuda_bf16.h>
 
+#include <type_traits>
+
 #include "device_common.cuh"
 #include "sparse24_pack.cuh"
 
@@ -91,6 +93,9 @@ struct GgProblem {
   int band;               // row tiles per band of the tile order
   int pair_rows;          // != 0: D's row r is stored at row (r & 1) * pair_rows + r / 2
   int a_mn;               // A is MN-major
+  int a_rows;             // rows of a K-major A's boxes: 128, or fewer tokens rounded up to 8
+  int t_rows;             // rows of the boxes that run along the contraction: 64, or a
+                          // shorter contraction rounded up to 16
   int by_sector;          // D is 32-byte aligned
   uint32_t idesc;
 };
@@ -192,20 +197,26 @@ struct GgWalk {
 // items in flight at a time form a block of D about as tall as wide and share
 // the operand stages they read through L2.
 __device__ __forceinline__ void gg_item(const GgProblem& p, int i, int& mt, int& nt, int& sp) {
-  const int tiles = p.m_tiles * p.n_tiles;
-  sp = i / tiles;
-  const int t = i - sp * tiles;
-  const int per_band = p.band * p.n_tiles;
-  const int b = t / per_band;
-  const int r = t - b * per_band;
-  const int m0 = b * p.band;
-  const int bsize = p.m_tiles - m0 < p.band ? p.m_tiles - m0 : p.band;
-  nt = r / bsize;
-  mt = m0 + (r - nt * bsize);
+  const uint32_t tiles = static_cast<uint32_t>(p.m_tiles * p.n_tiles);
+  const uint32_t s = p.splits == 1 ? 0 : static_cast<uint32_t>(i) / tiles;
+  const uint32_t t = static_cast<uint32_t>(i) - s * tiles;
+  const uint32_t per_band = static_cast<uint32_t>(p.band * p.n_tiles);
+  const uint32_t b = t / per_band;
+  const uint32_t r = t - b * per_band;
+  const uint32_t m0 = b * static_cast<uint32_t>(p.band);
+  const uint32_t left = static_cast<uint32_t>(p.m_tiles) - m0;
+  const uint32_t bsize = left < static_cast<uint32_t>(p.band) ? left : p.band;
+  const uint32_t n = r / bsize;
+  sp = static_cast<int>(s);
+  nt = static_cast<int>(n);
+  mt = static_cast<int>(m0 + (r - n * bsize));
 }
 
+// The product stays below 2^31: at most 2^25 stages and 32 splits.
 __device__ __forceinline__ int gg_first_stage(const GgProblem& p, int sp) {
-  return static_cast<int>(static_cast<long long>(p.stages_total) * sp / p.splits);
+  if (p.splits == 1) return sp == 0 ? 0 : p.stages_total;
+  return static_cast<int>(static_cast<uint32_t>(p.stages_total) * static_cast<uint32_t>(sp) /
+                          static_cast<uint32_t>(p.splits));
 }
 
 template <int BN>
@@ -277,6 +288,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
         int mt, nt, sp;
         gg_item(pr, index, mt, nt, sp);
         const int s1 = gg_first_stage(pr, sp + 1);
+        const int tile0 = mt * kGgTileM;
+        const int m0 = tile0 + static_cast<int>(rank) * 128;
+        const int n0 = nt * BN + static_cast<int>(rank) * (BN / 2);
+        const CUtensorMap* ta = &maps.a[which];
+        const CUtensorMap* tb = &maps.b[which];
+        // boxes of this CTA's A (a K-major one past the last row is left out:
+        // what D's rows there become is not stored); the pair's bytes a stage
+        const bool a_mn = pr.a_mn != 0;
+        const bool load_a = a_mn || m0 < pr.rows;
+        const uint32_t t_bytes = pr.t_rows * kGgChunk;
+        const uint32_t stage_bytes =
+            BN / 64 * t_bytes +
+            (a_mn ? 4 * t_bytes : (tile0 + 128 < pr.rows ? 2u : 1u) * pr.a_rows * kGgChunk);
         for (int u = gg_first_stage(pr, sp); u < s1; ++u, ++i) {
           if (i % P != warp) continue;
           const int stage = static_cast<int>(i % S);
@@ -286,20 +310,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
             ok = false;
             break;
           }
-          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), 2 * SB);
+          if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full_bar[stage]), stage_bytes);
           const uint32_t full = map_to_cta(smem_u32(&full_bar[stage]), 0);
           const uint32_t a_dst = smem_u32(stage_base + stage * SB);
           const uint32_t b_dst = a_dst + Cfg::kABytes;
-          const int m0 = mt * kGgTileM + static_cast<int>(rank) * 128;
-          const int n0 = nt * BN + static_cast<int>(rank) * (BN / 2);
           const int t0 = u * kGgStageK;
-          const CUtensorMap* ta = &maps.a[which];
-          const CUtensorMap* tb = &maps.b[which];
-          if (pr.a_mn) {
+          if (a_mn) {
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               tma_load_2d_pair(a_dst + h * kGgStageK * kGgChunk, ta, m0 + 64 * h, t0, full, pol);
-          } else {
+          } else if (load_a) {
             tma_load_2d_pair(a_dst, ta, t0, m0, full, pol);
           }
 #pragma unroll
@@ -330,9 +350,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
       int which, index;
       while (ok && walk.next(p, which, index)) {
         const GgProblem& pr = p.prob[which];
-        const int sp = index / (pr.m_tiles * pr.n_tiles);
+        const int sp = pr.splits == 1 ? 0 : index / (pr.m_tiles * pr.n_tiles);
         const int count = gg_first_stage(pr, sp + 1) - gg_first_stage(pr, sp);
         const uint32_t idesc = pr.idesc;
+        const int steps = pr.t_rows / 16;
         // K-major: 8-row groups 1024 bytes apart, 16 t = 32 bytes on.
         // MN-major: 64-wide chunks kGgStageK rows apart (leading offset),
         // groups of 8 t 1024 bytes apart, 16 t = two groups on.
@@ -341,27 +362,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGgThreads, 1)
         if (!mbar_wait_cluster_warp(smem_u32(&acce_bar[acc]), acc_phase ^ 1u, abort_flag)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * BN;
-        for (int u = 0; u < count; ++u) {
-          if (!ready && !mbar_wait_warp(smem_u32(&full_bar[stage]), phase, abort_flag)) {
-            ok = false;
-            break;
-          }
+        // One stage's products: all four 16-wide steps along the contraction, or `steps`.
+        auto take_stage = [&](auto whole, bool first) {
+          if (!ready && !mbar_wait_warp(smem_u32(&full_bar[stage]), phase, abort_flag)) return false;
           tc_fence_after();
           const int next_stage = stage + 1 == S ? 0 : stage + 1;
           const uint32_t next_phase = stage + 1 == S ? phase ^ 1u : phase;
           const uint32_t a_addr = smem_u32(stage_base + stage * SB);
           const uint32_t b_addr = a_addr + Cfg::kABytes;
+          const int n = decltype(whole)::value ? kGgStageK / 16 : steps;
 #pragma unroll
-          for (int j = 0; j < kGgStageK / 16; ++j) {
+          for (int j = 0; j < n; ++j) {
             const uint64_t adesc = smem_desc(a_addr + j * a_step, a_lbo, 1024, kSwizzle128);
             const uint64_t bdesc =
                 smem_desc(b_addr + j * 2048, kGgStageK * kGgChunk, 1024, kSwizzle128);
-            mma_bf16_pair_w(d_tmem, adesc, bdesc, idesc, (u > 0 || j > 0) ? 1u : 0u);
+            mma_bf16_pair_w(d_tmem, adesc, bdesc, idesc, (!first || j > 0) ? 1u : 0u);
             if (j == 0) ready = mbar_test_warp(smem_u32(&full_bar[next_stage]), next_phase);
           }
           tc_commit_pair_mc_w(smem_u32(&empty_bar[stage]), 0x3);
           stage = next_stage;
           phase = next_phase;
+          return true;
+        };
+        if (steps == kGgStageK / 16) {
+          for (int u = 0; ok && u < count; ++u) ok = take_stage(std::true_type{}, u == 0);
+        } else {
+          ok = take_stage(std::false_type{}, true);   // a contraction below one stage
         }
         if (!ok) break;
         tc_commit_pair_mc_w(smem_u32(&accf_bar[acc]), 0x3);
