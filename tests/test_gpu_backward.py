@@ -90,6 +90,10 @@ GATED = [(1, 1, 128), (3, 60, 256), (32, 100, 384), (100, 333, 128), (250, 705, 
 @pytest.mark.parametrize("m,n,k", GATED)
 @pytest.mark.parametrize("name,bias", [("silu", False), ("gelu", True)])
 def test_gated_backward(m, n, k, name, bias):
+    check_gated_backward(m, n, k, name, bias)
+
+
+def check_gated_backward(m, n, k, name, bias):
     a_q, s_a, codes, s_w, packed = operands(m, 2 * n, k, m + n + k)
     b = None
     if bias:
@@ -105,6 +109,37 @@ def test_gated_backward(m, n, k, name, bias):
     order = torch.cat((torch.arange(0, 2 * n, 2), torch.arange(1, 2 * n, 2))).cuda()
     refs = [refs[0], tuple(t[order] for t in refs[1]), tuple(t[order] for t in refs[2])]
     within(got, refs)
+
+
+# Few tokens: tiles and stages of which only some rows exist.
+FEW = [(1, 16389, 128), (2, 1003, 2176), (7, 16390, 128), (8, 3280, 640), (9, 1003, 2176),
+       (16, 823, 2560), (17, 2051, 1152), (31, 16387, 128), (32, 1640, 1280), (33, 1640, 1280),
+       (48, 300, 384), (63, 50, 256), (120, 16, 256), (121, 5, 640),
+       (5, 1638, 1280)]
+
+
+@pytest.mark.parametrize("m,n,k", FEW)
+def test_few_tokens(m, n, k):
+    a_fmt, w_fmt = ("e4m3", "e5m2") if m % 2 else ("e5m2", "e4m3")
+    a_q, s_a, codes, s_w, packed = operands(m, n, k, m + n, a_fmt, w_fmt)
+    # rows that end with the allocation, NaN between them
+    ld = (n + 7) // 8 * 8 + 8
+    flat = torch.full(((m - 1) * ld + n,), float("nan"), device="cuda", dtype=torch.bfloat16)
+    dy = flat.as_strided((m, n), (ld, 1))
+    dy.copy_(torch.randn(m, n, device="cuda", generator=gen(9)))
+    got = S.sfp8_sparse_linear_backward(dy, a_q, a_fmt, s_a, packed, w_fmt, s_w, n, k,
+                                        need_dbias=True)
+    d = dy.double()
+    within(got, backward_reference(d, torch.zeros_like(d), decode(a_q, a_fmt), s_a,
+                                   decode(codes, w_fmt), s_w))
+    alone = S.sfp8_sparse_linear_backward(dy, a_q, a_fmt, s_a, packed, w_fmt, s_w, n, k,
+                                          need_dw=False)
+    assert torch.equal(alone[0], got[0])
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 8195, 128), (6, 1026, 1152), (24, 826, 1280)])
+def test_few_tokens_gated(m, n, k):
+    check_gated_backward(m, n, k, "gelu", True)
 
 
 @pytest.mark.parametrize("name", ["silu", "gelu"])
