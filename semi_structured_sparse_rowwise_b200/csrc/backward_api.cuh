@@ -168,7 +168,7 @@ struct BackwardPlan {
   size_t dz_off, what_off, xhat_off, partial_off, sums_off, total;
 };
 
-constexpr int64_t kColSumMinRows = 64;   // rows a run at least
+constexpr int64_t kColSumMinRows = 32;   // rows a run at least: four for each of a block's warps
 
 size_t up256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 
@@ -187,7 +187,7 @@ BackwardPlan backward_plan(int64_t m, int64_t rows, int64_t k, bool keep_dz, int
   b.runs = sum_runs;
   if (sum_runs == 0) {
     const int64_t cols = (rows + kColSumCols - 1) / kColSumCols;
-    int64_t runs = (static_cast<int64_t>(num_sms) * 4 + cols - 1) / cols;
+    int64_t runs = (static_cast<int64_t>(num_sms) * 3 + cols - 1) / cols;
     const int64_t most = (m + kColSumMinRows - 1) / kColSumMinRows;
     if (runs > most) runs = most;
     b.runs = static_cast<int>(runs < 1 ? 1 : runs);
@@ -254,7 +254,10 @@ sfp8_status launch_prologue(DeviceInfo* dev, const BackwardPlan& bp, const Backw
   auto units = [&](int64_t r) { return (r + kExpandRows - 1) / kExpandRows * (c.k / 128); };
   if (c.dx != nullptr) p.blocks[0] = blocks_for(units(c.rows), 1, dev, 8);
   if (c.dw != nullptr) p.blocks[1] = blocks_for(units(c.m), 1, dev, 8);
-  if (copy) p.blocks[2] = blocks_for(c.m, 1, dev, 8);
+  if (copy) {
+    while (p.copy_shift < 8 && (int64_t(8) << p.copy_shift) < bp.ld_dz) ++p.copy_shift;
+    p.blocks[2] = blocks_for(c.m, 256 >> p.copy_shift, dev, 8);
+  }
   if (sums)
     p.blocks[3] = static_cast<int>((c.rows + kColSumCols - 1) / kColSumCols) * bp.runs;
   const int64_t blocks = static_cast<int64_t>(p.blocks[0]) + p.blocks[1] + p.blocks[2] +

@@ -574,6 +574,7 @@ struct PrologueParams {
   long long ld_dy;
   __nv_bfloat16* copy;
   long long ld_copy;
+  int copy_shift;               // log2 of the threads that copy a row
   // 3: column sums of dy over runs of rows
   float* sums;                  // [runs][rows]
   int runs, sums_by_16;         // sums_by_16: dy's rows may be read 16 bytes at a time
@@ -666,12 +667,15 @@ __device__ __forceinline__ void expand_rows(const PrologueParams& p, int block) 
 }
 
 // dy to rows of ld_copy elements (a multiple of 8), for a dy whose base or
-// row stride TMA cannot take; zeros past its columns.  A row per block and
-// step, 8 elements a thread.
+// row stride TMA cannot take; zeros past its columns.  8 elements a thread, a
+// row (or 2048 columns of one) by 1 << copy_shift threads.
 __device__ __forceinline__ void copy_dy(const PrologueParams& p, int block) {
-  for (long long r = block; r < p.m; r += p.blocks[2]) {
+  const int width = 1 << p.copy_shift, per_step = 256 >> p.copy_shift;
+  const int tx = threadIdx.x & (width - 1), ty = threadIdx.x >> p.copy_shift;
+  for (long long r = static_cast<long long>(block) * per_step + ty; r < p.m;
+       r += static_cast<long long>(p.blocks[2]) * per_step) {
     const unsigned short* src = reinterpret_cast<const unsigned short*>(p.dy) + r * p.ld_dy;
-    for (long long c = threadIdx.x * 8; c < p.ld_copy; c += 256 * 8) {
+    for (long long c = tx * 8; c < p.ld_copy; c += width * 8) {
       uint32_t v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = c + j < p.rows ? __ldg(src + c + j) : 0u;
