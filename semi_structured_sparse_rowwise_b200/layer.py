@@ -22,6 +22,21 @@ import torch
 from . import binding as B
 
 
+def _kept_workspace(cache, key, new, *sizes):
+    """cache[key], a forward workspace made by new(*sizes) when it is missing or
+    the library's algorithm table has changed since (which may pick a split that
+    needs a larger one, with its counters elsewhere).  One made inside a graph
+    capture is not kept: its clearing is part of the graph and has not run when
+    the capture ends, and its memory is the graph's."""
+    epoch = B.algo_epoch()
+    hit = cache.get(key)
+    if hit is None or hit[0] != epoch:
+        hit = (epoch, new(*sizes))
+        if not torch.cuda.is_current_stream_capturing():
+            cache[key] = hit
+    return hit[1]
+
+
 class SparseFp8Linear:
     """y = (s_a s_w^T) * (A_q W_q^T) + bias with a 2:4 compressed FP8 weight."""
 
@@ -60,16 +75,8 @@ class SparseFp8Linear:
     def workspace(self, m):
         """The layer's zeroed workspace for m tokens (kept between calls; each
         call leaves its split-K counters at zero).  Re-sized after any change
-        of the library's algorithm table (which may pick a split that needs a
-        larger one)."""
-        epoch = B.algo_epoch()
-        hit = self._ws.get(m)
-        if hit is None or hit[0] != epoch:
-            # a fresh zeroed buffer: another split keeps its counters elsewhere
-            ws = B.new_quant_workspace(m, self.n, self.k, self.device)
-            self._ws[m] = (epoch, ws)
-            return ws
-        return hit[1]
+        of the library's algorithm table."""
+        return _kept_workspace(self._ws, m, B.new_quant_workspace, m, self.n, self.k, self.device)
 
     def autotune(self, x, reps=10, flush_bytes=256 << 20):
         """Times every work split of the GEMM for x's token count on this
@@ -195,13 +202,8 @@ class SparseFp8GatedLinear:
         if kind == "backward":
             return _kept(self._ws, (kind, m), B.new_gated_backward_workspace, m, self.n, self.k,
                          self.device)
-        # a changed algorithm table may ask for another size
-        epoch = B.algo_epoch()
-        hit = self._ws.get((kind, m))
-        if hit is None or hit[0] != epoch:
-            new = B.new_gated_quant_workspace if kind == "quant" else B.new_gated_workspace
-            hit = self._ws[(kind, m)] = (epoch, new(m, self.n, self.k, self.device))
-        return hit[1]
+        new = B.new_gated_quant_workspace if kind == "quant" else B.new_gated_workspace
+        return _kept_workspace(self._ws, (kind, m), new, m, self.n, self.k, self.device)
 
     def forward_checkpoint(self, x, out=None):
         """(h [m, hidden] bf16, checkpoint) from x [m, k] bf16/f16/f32; the

@@ -1,0 +1,84 @@
+"""GPU tests of the workspaces that layers keep or take for a call: first used
+inside a graph capture, after a change of the algorithm table, for many token
+counts and on several streams."""
+import pytest
+import torch
+
+import semi_structured_sparse_rowwise_b200 as S
+from ffn_reference import gen
+from gpu_pipeline import ensure_library, requires_gpu
+
+pytestmark = [pytest.mark.gpu, requires_gpu]
+
+# few weight rows and a long k: the split forms, whose counters have to start at zero
+M, N, K = 16, 128, 8192
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    ensure_library()
+    yield
+    assert S.sfp8_read_device_status(clear=True) == (0, 0)
+
+
+def normal(seed, *shape):
+    return torch.randn(*shape, device="cuda", generator=gen(seed)).to(torch.bfloat16)
+
+
+def linear():
+    return S.SparseFp8Linear(normal(1, N, K)), lambda layer, x, out: layer(x, out=out)
+
+
+def gated():
+    return (S.SparseFp8GatedLinear(normal(1, N, K), normal(2, N, K)),
+            lambda layer, x, out: layer(x, out=out))
+
+
+def gated_codes():
+    layer, _ = gated()
+
+    def run(layer, x, out):
+        a_q, s_a = S.sfp8_quantize_rowwise(x, "e4m3")
+        return layer.forward_codes(a_q, s_a, out=out)
+
+    return layer, run
+
+
+FORWARDS = [linear, gated, gated_codes]
+
+
+def rows(make):
+    return N if make is linear else 2 * N
+
+
+def nan(*shape):
+    return torch.full(shape, float("nan"), device="cuda", dtype=torch.bfloat16)
+
+
+@pytest.mark.parametrize("make", FORWARDS)
+def test_first_call_inside_a_capture(make):
+    """The clearing of a workspace made during a capture is recorded, not run:
+    no later eager call may find that workspace."""
+    layer, run = make()
+    x = normal(3, M, K)
+    want = run(make()[0], x, None)
+    # memory of the graph's pool that holds something
+    pool, side = torch.cuda.graph_pool_handle(), torch.cuda.Stream()
+    filler, graph = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(filler, pool=pool, stream=side):
+        t = [torch.full((size << 20,), 255, dtype=torch.uint8, device="cuda")
+             for size in [1] * 16 + [32]]       # small blocks and a large one
+        del t
+    filler.replay()
+    torch.cuda.synchronize()
+    captured = nan(M, N)
+    with torch.cuda.graph(graph, pool=pool, stream=side):
+        run(layer, x, captured)
+    eager = run(layer, x, nan(M, N))       # before the graph's first run
+    torch.cuda.synchronize()
+    assert torch.equal(eager, want)
+    for _ in range(2):
+        captured.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(captured, want)
