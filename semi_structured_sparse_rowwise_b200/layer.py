@@ -27,13 +27,19 @@ def _kept_workspace(cache, key, new, *sizes):
     the library's algorithm table has changed since (which may pick a split that
     needs a larger one, with its counters elsewhere).  One made inside a graph
     capture is not kept: its clearing is part of the graph and has not run when
-    the capture ends, and its memory is the graph's."""
+    the capture ends, and its memory is the graph's.  One that a captured call
+    takes stays allocated as long as the cache, for the graph's replays, also
+    when the table changes."""
     epoch = B.algo_epoch()
-    hit = cache.get(key)
+    capturing = torch.cuda.is_current_stream_capturing()
+    hit = cache.get(key)        # table's state, workspace, those that graphs use
     if hit is None or hit[0] != epoch:
-        hit = (epoch, new(*sizes))
-        if not torch.cuda.is_current_stream_capturing():
-            cache[key] = hit
+        ws = new(*sizes)
+        if capturing:
+            return ws
+        hit = cache[key] = (epoch, ws, [] if hit is None else hit[2])
+    if capturing and all(ws is not hit[1] for ws in hit[2]):
+        hit[2].append(hit[1])
     return hit[1]
 
 

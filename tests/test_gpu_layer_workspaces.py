@@ -82,3 +82,35 @@ def test_first_call_inside_a_capture(make):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(captured, want)
+
+
+@pytest.mark.parametrize("make", FORWARDS)
+def test_captured_call_keeps_its_workspace_after_a_table_change(make):
+    layer, run = make()
+    x = normal(3, M, K)
+    want = run(layer, x, None).clone()
+    captured = nan(M, N)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        run(layer, x, captured)
+    n = rows(make)
+    query = (S.sfp8_sparse_linear_workspace_bytes if make is gated_codes else
+             S.sfp8_sparse_linear_quant_workspace_bytes)
+    try:
+        size = query(M, n, K)
+        # an entry that needs a workspace of another size: the old one's memory
+        # is not given to the new one
+        for algo in range(S.sfp8_sparse_linear_algo_count(M, n, K)):
+            S.sfp8_sparse_linear_set_algo(M, n, K, algo)
+            if (query(M, n, K) + 511) // 512 != (size + 511) // 512:
+                break
+        run(layer, x, None)                # the layer's workspace follows the table
+        torch.cuda.synchronize()
+        taken = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(bool((t == 255).all()) for t in taken)
+        assert torch.equal(captured, want)
+    finally:
+        S.sfp8_sparse_linear_set_algo(M, n, K, 0)
