@@ -10,6 +10,7 @@ allocate their outputs with torch when none are given.
 """
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -732,6 +733,21 @@ def _new_workspace(query, sizes, device):
     return torch.zeros((max(nbytes, 16),), dtype=torch.uint8, device=device)
 
 
+@functools.lru_cache(maxsize=4096)
+def _scratch_bytes(query, sizes, index):
+    with torch.cuda.device(index):
+        return max(int(getattr(load_library(), query)(*sizes)), 16)
+
+
+def _new_scratch(query, sizes, device):
+    """A workspace that needs no clearing; its size is a matter of the call's
+    sizes and the device only, and is asked for once."""
+    index = torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    return torch.empty((_scratch_bytes(query, sizes, index),), dtype=torch.uint8, device=device)
+
+
 # ---- gated block
 
 
@@ -818,14 +834,12 @@ def sfp8_gated_linear_quant(x, a_dtype, packed, w_dtype, s_w, n, k, act="silu", 
 
 def new_linear_backward_workspace(m, n, k, device):
     """A workspace for sfp8_sparse_linear_backward(m, n, k) on `device`."""
-    return _new_workspace(load_library().sfp8_sparse_linear_backward_workspace_bytes, (m, n, k),
-                          device)
+    return _new_scratch("sfp8_sparse_linear_backward_workspace_bytes", (m, n, k), device)
 
 
 def new_gated_backward_workspace(m, n, k, device):
     """A workspace for sfp8_gated_linear_backward(m, n, k) on `device`."""
-    return _new_workspace(load_library().sfp8_gated_linear_backward_workspace_bytes, (m, n, k),
-                          device)
+    return _new_scratch("sfp8_gated_linear_backward_workspace_bytes", (m, n, k), device)
 
 
 def _gradient(t, wanted, what, shape, like):
@@ -952,8 +966,7 @@ def sfp8_layernorm_quant(x, weight=None, bias=None, eps=1e-5, q_dtype="e4m3", q=
 
 def new_layernorm_backward_workspace(rows, cols, device):
     """A workspace for sfp8_layernorm_backward on `device`."""
-    return _new_workspace(load_library().sfp8_layernorm_backward_workspace_bytes, (rows, cols),
-                          device)
+    return _new_scratch("sfp8_layernorm_backward_workspace_bytes", (rows, cols), device)
 
 
 def sfp8_layernorm_backward(dy, x, weight, mean, rstd, dx=None, dweight=None, dbias=None,

@@ -114,3 +114,19 @@ def test_captured_call_keeps_its_workspace_after_a_table_change(make):
         assert torch.equal(captured, want)
     finally:
         S.sfp8_sparse_linear_set_algo(M, n, K, 0)
+
+
+def test_workspaces_that_need_no_clearing_are_not_cleared(monkeypatch):
+    def cleared(*_, **__):
+        raise AssertionError("cleared")
+
+    made = (S.new_linear_backward_workspace, (300, 500, 256), S.new_gated_backward_workspace,
+            (300, 500, 256), S.new_layernorm_backward_workspace, (300, 500))
+    sizes = [f(*a, "cuda").numel() for f, a in zip(made[0::2], made[1::2])]
+    monkeypatch.setattr(torch, "zeros", cleared)
+    assert [f(*a, "cuda").numel() for f, a in zip(made[0::2], made[1::2])] == sizes
+    monkeypatch.undo()
+    # the forward's have to start at zero
+    for f in (S.new_gated_workspace, S.new_gated_quant_workspace, S.new_workspace,
+              S.new_quant_workspace):
+        assert not bool(f(M, N, K, "cuda").any())
