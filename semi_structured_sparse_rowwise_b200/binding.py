@@ -871,7 +871,8 @@ def sfp8_sparse_linear_backward(dy, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, 
     dw = _gradient(dw, need_dw, "dw", (n, k), dy)
     dbias = _gradient(dbias, need_dbias, "dbias", (n,), dy)
     if workspace is None:
-        workspace = new_linear_backward_workspace(m, n, k, dev)
+        workspace = a_q.new_empty(
+            _scratch_bytes("sfp8_sparse_linear_backward_workspace_bytes", (m, n, k), dev.index))
     _run("sfp8_sparse_linear_backward", dev, dy.data_ptr(), ld, a_q.data_ptr(), _fp8(a_dtype),
          s_a.data_ptr(), m, packed.data_ptr(), _fp8(w_dtype), s_w.data_ptr(), n, k, _addr(dx),
          _addr(dw), _addr(dbias), *_workspace(workspace, dev))
@@ -894,7 +895,8 @@ def sfp8_gated_linear_backward(dh, a_q, a_dtype, s_a, packed, w_dtype, s_w, n, k
     dw = _gradient(dw, need_dw, "dw", (2 * n, k), dh)
     dbias = _gradient(dbias, need_dbias, "dbias", (2 * n,), dh)
     if workspace is None:
-        workspace = new_gated_backward_workspace(m, n, k, dev)
+        workspace = a_q.new_empty(
+            _scratch_bytes("sfp8_gated_linear_backward_workspace_bytes", (m, n, k), dev.index))
     _run("sfp8_gated_linear_backward", dev, dh.data_ptr(), ld, a_q.data_ptr(), _fp8(a_dtype),
          s_a.data_ptr(), m, packed.data_ptr(), _fp8(w_dtype), s_w.data_ptr(), n, k,
          _activation(act), _addr(bias), _addr(dx), _addr(dw), _addr(dbias),

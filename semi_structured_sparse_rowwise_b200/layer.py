@@ -14,7 +14,10 @@ norm, gated block, down projection).  Their ``forward_checkpoint`` returns what
 the backward pass needs beside the result: the quantised activation and its
 scales, one byte per element.  Gradients are straight-through: those of the
 weights that were prepared, dense, for the caller's optimiser, whose updated
-weights make new layers.
+weights make new layers.  A backward pass takes its workspace from torch's
+allocator for the call (0.8 GB for a gated block of 14336 units over 4096 at 8192
+tokens), so layers, token counts and streams share one and any number of passes
+may be in flight.
 """
 
 import torch
@@ -138,9 +141,7 @@ class SparseFp8Linear:
             need_dbias = self.bias is not None
         return B.sfp8_sparse_linear_backward(
             dy, a_q, self.a_dtype, s_a, self.packed, self.w_dtype, self.s_w, self.n, self.k,
-            need_dx=need_dx, need_dw=need_dw, need_dbias=need_dbias,
-            workspace=_kept(self._ws, ("backward", a_q.shape[0]), B.new_linear_backward_workspace,
-                            a_q.shape[0], self.n, self.k, self.device))
+            need_dx=need_dx, need_dw=need_dw, need_dbias=need_dbias)
 
     def _act_buffers(self, m):
         """The quantised activation [m, k] and its scales [m] (kept per m)."""
@@ -176,14 +177,6 @@ class SparseFp8Linear:
             self.workspace(m), bias=self.bias)
 
 
-def _kept(cache, key, new, *sizes):
-    """cache[key], made by new(*sizes) when it is missing."""
-    ws = cache.get(key)
-    if ws is None:
-        ws = cache[key] = new(*sizes)
-    return ws
-
-
 class SparseFp8GatedLinear:
     """h = act(x W_gate^T + b_gate) * (x W_up^T + b_up) over one compressed weight
     that holds both, one kernel for the whole block."""
@@ -205,9 +198,6 @@ class SparseFp8GatedLinear:
         self._ws = {}
 
     def _workspace(self, kind, m):
-        if kind == "backward":
-            return _kept(self._ws, (kind, m), B.new_gated_backward_workspace, m, self.n, self.k,
-                         self.device)
         new = B.new_gated_quant_workspace if kind == "quant" else B.new_gated_workspace
         return _kept_workspace(self._ws, (kind, m), new, m, self.n, self.k, self.device)
 
@@ -246,7 +236,7 @@ class SparseFp8GatedLinear:
         dx, dw, db = B.sfp8_gated_linear_backward(
             dh, a_q, self.a_dtype, s_a, self.packed, self.w_dtype, self.s_w, self.n, self.k,
             act=self.act, bias=self.bias, need_dx=need_dx, need_dw=need_dw,
-            need_dbias=need_dbias, workspace=self._workspace("backward", a_q.shape[0]))
+            need_dbias=need_dbias)
         return (dx, None if dw is None else dw.view(2, self.n, self.k),
                 None if db is None else db.view(2, self.n))
 
@@ -263,7 +253,6 @@ class SparseFp8FeedForward:
         self.down = SparseFp8Linear(w_down, w_dtype=w_dtype, a_dtype=a_dtype)
         if self.down.k != self.gated.n:
             raise ValueError("w_down must have one column per hidden unit")
-        self._ws = {}
 
     def forward_checkpoint(self, x):
         """(y [m, out] bf16, checkpoint) from x [m, k]; the checkpoint keeps x
@@ -289,11 +278,7 @@ class SparseFp8FeedForward:
         dn, dw, _ = self.gated.backward(dh, outer)
         # the norm's backward pass takes its gradient in x's type
         dn = dn if dn.dtype == x.dtype else dn.to(x.dtype)
-        rows, cols = x.shape
-        dx, d_weight, d_bias = B.sfp8_layernorm_backward(
-            dn, x, self.norm_weight, mean, rstd,
-            workspace=_kept(self._ws, rows, B.new_layernorm_backward_workspace, rows, cols,
-                            x.device))
+        dx, d_weight, d_bias = B.sfp8_layernorm_backward(dn, x, self.norm_weight, mean, rstd)
         return dict(dx=dx, norm_weight=d_weight, norm_bias=d_bias, w_gate=dw[0], w_up=dw[1],
                     w_down=dw_down)
 

@@ -130,3 +130,58 @@ def test_workspaces_that_need_no_clearing_are_not_cleared(monkeypatch):
     for f in (S.new_gated_workspace, S.new_gated_quant_workspace, S.new_workspace,
               S.new_quant_workspace):
         assert not bool(f(M, N, K, "cuda").any())
+
+
+def backward_layers():
+    k, hidden = 256, 384
+    w = dict(norm_weight=normal(1, k), norm_bias=normal(2, k), w_gate=normal(3, hidden, k),
+             w_up=normal(4, hidden, k), w_down=normal(5, k, hidden))
+    block = S.SparseFp8FeedForward(**w)
+    return {"linear": (block.down, hidden, k), "gated": (block.gated, k, hidden),
+            "block": (block, k, k)}
+
+
+def tensors(out):
+    return [t for t in (out.values() if isinstance(out, dict) else out) if t is not None]
+
+
+@pytest.mark.parametrize("kind", ["linear", "gated", "block"])
+def test_backward_leaves_no_memory_behind(kind):
+    """Nothing in a backward pass's workspace is needed after the call, so the
+    layer holds none, however many token counts it has met."""
+    layer, k, n = backward_layers()[kind]
+    held = []
+    for m in (65, 130, 300, 301, 512, 777):
+        x, dy = normal(m, m, k), normal(m + 1, m, n)
+        _, ckpt = layer.forward_checkpoint(x)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        grads = layer.backward(dy, ckpt)
+        torch.cuda.synchronize()
+        del grads, x, dy, ckpt
+        held.append(torch.cuda.memory_allocated() - before)
+    # with the step's tensors gone, less is allocated than before the call
+    assert all(h <= 0 for h in held), held
+
+
+@pytest.mark.parametrize("kind", ["linear", "gated", "block"])
+def test_backward_on_two_streams_at_once(kind):
+    layer, k, n = backward_layers()[kind]
+    m = 700
+    steps = []
+    for i in range(2):
+        _, ckpt = layer.forward_checkpoint(normal(10 + i, m, k))
+        steps.append((normal(20 + i, m, n), ckpt))
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in tensors(layer.backward(*s))] for s in steps]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in steps]
+    got = [[], []]
+    for _ in range(30):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(tensors(layer.backward(*steps[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
