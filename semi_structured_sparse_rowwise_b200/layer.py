@@ -298,16 +298,27 @@ class HostPipeline:
         dev = layer.device
         self.layer, self.m = layer, m
         self.streams = [torch.cuda.Stream(dev) for _ in range(3)]
-        ws = B.new_quant_workspace(m, layer.n, layer.k, dev)
-        self._ws_epoch = B.algo_epoch()
         self.slots = []
         for _ in range(depth):
             self.slots.append(dict(
                 x=torch.empty((m, layer.k), dtype=x_dtype, device=dev),
                 y=torch.empty((m, layer.n), dtype=torch.bfloat16, device=dev),
                 a_q=torch.empty((m, layer.k), dtype=torch.uint8, device=dev),
-                s_a=torch.empty((m,), dtype=torch.float32, device=dev), ws=ws))
+                s_a=torch.empty((m,), dtype=torch.float32, device=dev)))
+        self._new_workspace()
         self._reset()
+
+    def _new_workspace(self):
+        """A zeroed workspace for the table's present choice.  The pipeline's
+        streams come after what the current one has queued, the clearing and the
+        layer's preparation among it."""
+        L = self.layer
+        self._ws_epoch = B.algo_epoch()
+        ws = B.new_quant_workspace(self.m, L.n, L.k, L.device)
+        for sl in self.slots:
+            sl["ws"] = ws
+        for s in self.streams:
+            s.wait_stream(torch.cuda.current_stream(L.device))
 
     def _reset(self):
         for sl in self.slots:
@@ -329,10 +340,7 @@ class HostPipeline:
         if self._ws_epoch != B.algo_epoch():
             # the algorithm table changed: the forward may need a larger workspace
             self.synchronize()
-            ws = B.new_quant_workspace(self.m, L.n, L.k, L.device)
-            for s_ in self.slots:
-                s_["ws"] = ws
-            self._ws_epoch = B.algo_epoch()
+            self._new_workspace()
         # the set is free once its previous forward has read x and its
         # previous copy out has read y
         if sl["used"]:

@@ -185,3 +185,29 @@ def test_backward_on_two_streams_at_once(kind):
     for i in range(2):
         for g in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(g, want[i]))
+
+
+def host_batches(count):
+    xs = [normal(50 + i, M, K).cpu().pin_memory() for i in range(count)]
+    return xs, [torch.empty((M, N), dtype=torch.bfloat16).pin_memory() for _ in xs]
+
+
+def test_pipeline_waits_for_what_made_it():
+    """The pipeline's streams come after the work that the making stream still
+    has queued: its workspace's clearing, the layer's preparation."""
+    layer = S.SparseFp8Linear(normal(1, N, K))
+    xs, ys = host_batches(3)
+    want = [layer(x.cuda()).cpu() for x in xs]
+    size = S.sfp8_sparse_linear_quant_workspace_bytes(M, N, K)
+    torch.cuda.synchronize()
+    t = [torch.full((max(size, 16),), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    torch.cuda.synchronize()
+    del t
+    torch.cuda._sleep(400_000_000)         # keeps the current stream busy for a while
+    pipe = S.HostPipeline(layer, M, depth=2)
+    for x, y in zip(xs, ys):
+        y.fill_(float("nan"))
+        pipe.submit(x, y)
+    pipe.synchronize()
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, w) for y, w in zip(ys, want))
