@@ -369,6 +369,8 @@ class HostPipeline:
         belong to the graph afterwards: use another pipeline for eager
         submits."""
         self.synchronize()
+        if self._ws_epoch != B.algo_epoch():
+            self._new_workspace()     # now: nothing can be waited for during the capture
         self._reset()
         origin = torch.cuda.Stream(self.layer.device)
         origin.wait_stream(torch.cuda.current_stream(self.layer.device))

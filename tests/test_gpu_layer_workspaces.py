@@ -211,3 +211,21 @@ def test_pipeline_waits_for_what_made_it():
     pipe.synchronize()
     torch.cuda.synchronize()
     assert all(torch.equal(y, w) for y, w in zip(ys, want))
+
+
+def test_pipeline_captured_after_a_table_change():
+    layer = S.SparseFp8Linear(normal(1, N, K))
+    xs, ys = host_batches(3)
+    want = [layer(x.cuda()).cpu() for x in xs]
+    pipe = S.HostPipeline(layer, M, depth=2)
+    try:
+        S.sfp8_sparse_linear_set_algo(M, N, K, 0)      # counts as a change
+        graph = pipe.capture(xs, ys)
+        for _ in range(2):
+            for y in ys:
+                y.fill_(float("nan"))
+            graph.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(y, w) for y, w in zip(ys, want))
+    finally:
+        S.sfp8_sparse_linear_set_algo(M, N, K, 0)
