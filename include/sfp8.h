@@ -576,13 +576,15 @@ sfp8_status sfp8_gated_linear_backward(const void* dh, int64_t ld_dh, const void
  * y next to a border of the format may fall on either side of it.
  *
  *  x       device, [rows, cols] of x_dtype (BF16, F16 or F32), row stride
- *          ld_x >= cols.  cols >= 1, any; with q, cols % 16 == 0 and x as for
- *          sfp8_quantize_rowwise (16-byte aligned base and rows).  Rows that
- *          are 16-byte aligned (cols, ld_x and every buffer) are read 16
- *          bytes at a time.
+ *          ld_x >= cols.  cols >= 1, any.  Where x's base and rows, y, weight
+ *          and bias are 16-byte aligned and cols is a multiple of 16 bytes, rows
+ *          are read 16 bytes at a time, else by element; with q it is
+ *          SFP8_ERR_MISALIGNED where they are not, or q is not, and cols % 16
+ *          has to be 0.
  *  weight, bias  device, [cols] of p_dtype, which is x_dtype or F32, or NULL
- *          (ones, zeros); aligned to their element.
- *  eps     >= 0 and finite.  A constant row with eps 0 gives NaN (0 * inf).
+ *          (ones, zeros); aligned to their element (16 bytes with q).
+ *  eps     >= 0 and finite.  A constant row has no norm with eps 0: it gives
+ *          NaN (0 * inf) where the fp32 mean is exact, else noise.
  *  y       device, [rows, cols] of x_dtype, or NULL.
  *  q, q_dtype, scales  device, [rows, cols] codes and [rows] float32, or q
  *          NULL (scales and q_dtype are then not looked at).

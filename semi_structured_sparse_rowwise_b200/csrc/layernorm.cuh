@@ -21,8 +21,9 @@
 //   row kernel     few rows (or short ones): one row per group of TPR threads,
 //                  N vectors of VEC elements each in registers, reduced by
 //                  warp shuffles and, for more than one warp, shared memory.
-//   stream kernel  many rows of 1 to 16 KB: one persistent block a SM with
-//                  two to sixteen row groups of 64 to 256 threads.  Each group
+//   stream kernel  rows of 1 to 16 KB, forward where there are many, backward
+//                  any number: one persistent block a SM with two to fifteen
+//                  row groups of 64 to 256 threads.  Each group
 //                  has a ring of row buffers in shared memory that bulk
 //                  copies keep filled ahead, so that HBM streams through the
 //                  reductions' barriers; the parameters lie in shared memory
@@ -337,8 +338,6 @@ __global__ void __launch_bounds__(1024)
 // ------------------------------------------------------------------ row ring
 
 constexpr int kNormMaxSlots = 8;
-
-
 
 // Ring of row buffers of a row group: its rows go through the slots in turn
 // (`PARTS` rows of `bytes` each, from as many tensors), the group's position

@@ -30,16 +30,13 @@ int norm_slots(int groups, int params, int cols, int parts, int row_bytes) {
 }
 
 // Co-resident blocks of a persistent kernel on the device (queried once a
-// slot; `smem` is the same for every launch that uses the slot).
+// slot).
 template <typename Kernel>
-sfp8_status norm_resident(DeviceInfo* dev, int slot, Kernel kern, int threads, int smem,
-                          int* blocks) {
+sfp8_status norm_resident(DeviceInfo* dev, int slot, Kernel kern, int threads, int* blocks) {
   std::lock_guard<std::mutex> lock(g_mutex);
   if (dev->norm_blocks[slot] == 0) {
     int occ = 0;
-    if ((smem > 0 && cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          smem) != cudaSuccess) ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, smem) != cudaSuccess ||
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, kern, threads, 0) != cudaSuccess ||
         occ < 1) {
       cudaGetLastError();
       return SFP8_ERR_CUDA;
@@ -166,7 +163,7 @@ sfp8_status launch_norm_grad_rows(DeviceInfo* dev, int slot, NormGradParams& p, 
   constexpr int threads = TPR == 32 ? 256 : TPR;
   constexpr int per_block = TPR == 32 ? 8 : 1;
   int blocks = 0;
-  const sfp8_status s = norm_resident(dev, slot, kern, threads, 0, &blocks);
+  const sfp8_status s = norm_resident(dev, slot, kern, threads, &blocks);
   if (s != SFP8_OK) return s;
   // one wave of co-resident blocks
   if (p.groups > static_cast<int64_t>(blocks) * per_block) p.groups = blocks * per_block;

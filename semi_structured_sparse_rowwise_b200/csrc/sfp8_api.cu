@@ -36,7 +36,7 @@ struct DeviceInfo {
   bool smem_attr_set[80] = {};   // (BN, KS, RA, FQ) instantiations, then the gated ones
   int pair_clusters[12] = {};    // co-resident pairs of the pair kernel by (KS, WT) and epilogue
                                  // (0: unknown)
-  int grad_clusters[4] = {};     // the same of the gradient GEMM by (tile width, A's major-ness)
+  int grad_clusters[2] = {};     // the same of the gradient GEMM by tile width
   int norm_blocks[72] = {};      // co-resident CTAs per SM of the persistent layer norm kernels
                                  // by (direction, type, row split) (0: unknown)
   int tw_blocks[12] = {};        // co-resident CTAs per SM of the tensor-wise quantiser (0: unknown)

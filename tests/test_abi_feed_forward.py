@@ -193,3 +193,15 @@ def test_from_plain_c(lib, tmp_path):
                     "-Wl,-rpath," + os.path.dirname(so)], check=True)
     out = subprocess.run([str(exe)], capture_output=True, text=True)
     assert out.returncode == 0 and out.stdout == "abi ok\n", (out.returncode, out.stdout)
+
+
+def test_layernorm_to_codes_wants_aligned_parameters(lib):
+    """Codes are made 16 bytes at a time only: what is aligned to its element
+    alone is refused, as the header says."""
+    good = dict(x=FAKE, dtype=BF16, rows=4, cols=64, ld=64, weight=None, bias=None, p_dtype=F32,
+                eps=1e-5, y=None, q=ctypes.c_void_p(0x20000), q_dtype=E4M3,
+                scales=ctypes.c_void_p(0x30000), mean=None, rstd=None, stream=None)
+    f = lib.sfp8_layernorm
+    for name in ("x", "y", "q", "weight", "bias"):
+        assert call(f, good, **{name: ctypes.c_void_p(0x40008)}) == MISALIGNED
+    assert call(f, good, ld=68) == MISALIGNED
