@@ -125,7 +125,9 @@ class SparseFp8Linear:
     def forward_checkpoint(self, x):
         """The forward for training: (y, checkpoint), the checkpoint being the
         quantised activation [m, k] and its scales [m] in buffers of its own
-        (any number may be kept at a time), the input of ``backward``."""
+        (any number may be kept at a time), the input of ``backward``.  The
+        workspace is the layer's: one forward of a layer per token count in
+        flight at a time, as in ``forward``."""
         m = x.shape[0]
         y, a_q, s_a = B.sfp8_sparse_linear_quant(x, self.a_dtype, self.packed, self.w_dtype,
                                                  self.s_w, self.n, self.k, bias=self.bias,
@@ -179,7 +181,8 @@ class SparseFp8Linear:
 
 class SparseFp8GatedLinear:
     """h = act(x W_gate^T + b_gate) * (x W_up^T + b_up) over one compressed weight
-    that holds both, one kernel for the whole block."""
+    that holds both, one kernel for the whole block.  ``act`` is "silu" or "gelu",
+    the latter in its tanh form (torch's ``approximate="tanh"``)."""
 
     def __init__(self, w_gate, w_up, bias_gate=None, bias_up=None, act="silu", w_dtype="e4m3",
                  a_dtype="e4m3"):
@@ -204,10 +207,12 @@ class SparseFp8GatedLinear:
     def forward_checkpoint(self, x, out=None):
         """(h [m, hidden] bf16, checkpoint) from x [m, k] bf16/f16/f32; the
         checkpoint (codes and scales of x) is the input of ``backward``.  The
-        layer keeps one workspace per token count, so one call of a layer per
-        token count may be in flight at a time (calls on one stream are
-        ordered); calls captured in graphs that may run at the same time take
-        layers of their own."""
+        layer keeps one workspace per token count, so one forward call of a
+        layer per token count may be in flight at a time (calls on one stream
+        are ordered); calls captured in graphs that may run at the same time, or
+        beside eager ones, take layers of their own.  (A captured call uses the
+        workspace that eager calls have made; where there is none, one of the
+        graph's own that the graph clears at each run.)"""
         h, a_q, s_a = B.sfp8_gated_linear_quant(
             x, self.a_dtype, self.packed, self.w_dtype, self.s_w, self.n, self.k, act=self.act,
             bias=self.bias, out=out, workspace=self._workspace("quant", x.shape[0]))
@@ -243,8 +248,10 @@ class SparseFp8GatedLinear:
 
 class SparseFp8FeedForward:
     """The feed-forward sublayer without its residual addition:
-    y = down(act(gate(norm(x))) * up(norm(x))), the norm going straight to the
-    FP8 codes that the gated block reads."""
+    y = down(act(gate(norm(x))) * up(norm(x))), the norm, a layer norm, going
+    straight to the FP8 codes that the gated block reads.  One forward call per
+    token count may be in flight at a time, as for its two layers; backward
+    passes share nothing."""
 
     def __init__(self, norm_weight, norm_bias, w_gate, w_up, w_down, act="silu", eps=1e-5,
                  w_dtype="e4m3", a_dtype="e4m3"):
