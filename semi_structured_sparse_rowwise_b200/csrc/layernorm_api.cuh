@@ -157,9 +157,9 @@ int64_t norm_groups(int64_t rows, int num_sms) {
   return g < rows ? g : rows;
 }
 
-template <typename T, int VEC, int TPR, int N>
+template <typename T, int VEC, int TPR, int N, bool NARROW = false>
 sfp8_status launch_norm_grad_rows(DeviceInfo* dev, int slot, NormGradParams& p, cudaStream_t st) {
-  auto kern = layernorm_backward_kernel<T, VEC, TPR, N>;
+  auto kern = layernorm_backward_kernel<T, VEC, TPR, N, NARROW>;
   constexpr int threads = TPR == 32 ? 256 : TPR;
   constexpr int per_block = TPR == 32 ? 8 : 1;
   int blocks = 0;
@@ -227,6 +227,7 @@ sfp8_status launch_norm_grad(DeviceInfo* dev, int kind, NormGradParams& p, bool 
     if (nvec <= 1024)
       return go(5, layernorm_backward_stream_kernel<T, V, 256, 4, 512, false>, 512, 2);
   } else {
+    if (p.cols <= 32) return launch_norm_grad_rows<T, 1, 32, 1, true>(dev, 72 + kind, p, st);
     if (p.cols <= 1024) return launch_norm_grad_rows<T, 1, 128, 8>(dev, s0 + 6, p, st);
     if (p.cols <= 4096) return launch_norm_grad_rows<T, 1, 512, 8>(dev, s0 + 7, p, st);
   }

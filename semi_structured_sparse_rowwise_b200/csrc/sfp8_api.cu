@@ -37,7 +37,7 @@ struct DeviceInfo {
   int pair_clusters[12] = {};    // co-resident pairs of the pair kernel by (KS, WT) and epilogue
                                  // (0: unknown)
   int grad_clusters[2] = {};     // the same of the gradient GEMM by tile width
-  int norm_blocks[72] = {};      // co-resident CTAs per SM of the persistent layer norm kernels
+  int norm_blocks[75] = {};      // co-resident CTAs per SM of the persistent layer norm kernels
                                  // by (direction, type, row split) (0: unknown)
   int tw_blocks[12] = {};        // co-resident CTAs per SM of the tensor-wise quantiser (0: unknown)
   long long l2_bytes = 0;

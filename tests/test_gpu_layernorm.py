@@ -287,3 +287,29 @@ def test_refusals():
                     16, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(S.Sfp8Error):
             bad()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("cols", [1, 2, 3, 5, 31, 33])
+@pytest.mark.parametrize("rows", [1, 9, 3000])
+def test_backward_of_narrow_rows(rows, cols, dtype):
+    """A row of two has nothing left but eps once its mean and its slope are taken
+    out, 1e-5 of the terms: no digit of the fp32 terms' rounding may reach it.
+    Up to 32 columns, read by element, dx is the 64-bit value rounded to fp32 and once more to x's
+    type (2^-50 of the terms for 64-bit rounding, half of fp16's finest step)."""
+    x, w, b = inputs(rows, cols, dtype, rows + cols)
+    _, mean, rstd = S.sfp8_layernorm(x, w, b, EPS)
+    dy = torch.randn(rows, cols, device="cuda", generator=gen(4)).to(dtype)
+    got = S.sfp8_layernorm_backward(dy, x, w, mean, rstd)
+    check_backward(got, dy, x, w, mean, rstd, dtype)
+    if cols > 32:
+        return
+    r = rstd.double()[:, None]
+    xh = (x.double() - mean.double()[:, None]) * r
+    g = dy.double() * w.double()
+    a, c = g.mean(1, keepdim=True), xh * (g * xh).mean(1, keepdim=True)
+    ref = r * (g - a - c)
+    bound = (half_step(dtype) + 2.0 ** -23) * ref.abs() + 2.0 ** -50 * r * (
+        g.abs() + a.abs() + c.abs()) + (2.0 ** -25 if dtype == torch.float16 else 2.0 ** -140)
+    off = (got[0].double() - ref).abs()
+    assert bool((off <= bound).all()), float((off / bound).max())
