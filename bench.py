@@ -12,7 +12,10 @@ Llama-3.1-8B prefill linears at M=8192 (QKV, O, up, down; A with 1 % outlier
 channels), each in dense-equivalent TFLOP/s against 4 x the measured bf16
 peak, burst and sustained, then the dtype sweep (K=4096, N=14336, M in
 {1, 16, 128, 1024, 8192} x the four e4m3/e5m2 operand pairs) and the
-Llama-3-70B-shaped stress GEMM (16384 x 8192 x 28672).
+Llama-3-70B-shaped stress GEMM (16384 x 8192 x 28672).  The printed line is
+short (below 2000 characters, so that a reader of the output's last kilobytes
+has all of it): `per_workload` gives one or two figures a case, and notes on how
+a figure was taken are left out.  `--detail FILE` writes the whole record.
 
 A step is one forward of the layer: dynamic row-wise FP8 quantisation of the
 activation followed by the sparse FP8 GEMM with its scale epilogue (one
@@ -736,7 +739,10 @@ def run_ours(args):
                 "unit": "GB/s", "ms": t_prep * 1e3, "cores": cores, "kind": "oracle",
                 "sample": note}
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        if args.detail:
+            with open(args.detail, "w") as f:
+                json.dump(line, f, indent=1)
+        print(json.dumps(brief_line(line)), flush=True)
     del g_step, g_gemm, g_q
     if world > 1:
         import torch.distributed as dist
@@ -1096,6 +1102,48 @@ def run_matrix(args):
     return 0
 
 
+def _short(v):
+    """Numbers to five digits (whole ones stay), through lists and dicts."""
+    if isinstance(v, float):
+        return v if v.is_integer() else float("%.5g" % v)
+    if isinstance(v, dict):
+        return {k: _short(x) for k, x in v.items()}
+    if isinstance(v, list):
+        return [_short(x) for x in v]
+    return v
+
+
+def brief_line(line):
+    """The record as it is printed: every key, but notes left out and the cases
+    of `per_workload` as single figures (the linears: TFLOP/s and the fraction of
+    the measured peak, both sustained; the sweep: per M the e4m3 pair's GEMM
+    rate; the stress shape: TFLOP/s)."""
+    notes = {"timing", "step", "launches_timed", "peak_source", "path", "sample", "call", "seeds",
+             "replays", "peak_datasheet"}
+    out = {}
+    for key, v in line.items():
+        if isinstance(v, dict) and key != "per_workload":
+            v = _short({k: x for k, x in v.items() if k not in notes})
+        elif key not in ("value", "ms_per_step"):
+            v = _short(v)
+        out[key] = v
+    cases = line.get("per_workload")
+    if cases:
+        short = {}
+        for wl, c in cases.items():
+            if wl == "prefill_8b":
+                short[wl] = {p["shape"]: [p["TFLOP/s"], p["roofline"]["frac_sustained"]]
+                             for p in c}
+            else:
+                short[wl] = {}
+                for t in c["table"]:
+                    if (t["a"], t["w"]) == ("e4m3", "e4m3"):
+                        u = "GB/s" if "GB/s" in t else "TFLOP/s"
+                        short[wl].setdefault(u, {})["m=%d" % t["m"]] = t[u]
+        out["per_workload"] = _short(short)
+    return out
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -1117,6 +1165,8 @@ def main():
                     help="quantize_tensorwise: input dtypes, comma-separated (f32, bf16)")
     ap.add_argument("--impl", default="ours", choices=["ours", "reference"])
     ap.add_argument("--all-m", action="store_true", help="also time M=1 and M=4")
+    ap.add_argument("--detail", default="", help="also write the whole record (notes, every "
+                    "case of the tables) to this file")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--cpu-seconds", type=float, default=10.0)
     ap.add_argument("--cpu-seconds-matrix", type=float, default=1.0,
